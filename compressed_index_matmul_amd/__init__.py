@@ -17,6 +17,9 @@ Entry points (same names as the C ABI):
   (input side) or inverse (output side), in one launch
 * :func:`vq_gemv_rht`       -- vq_gemv with the input transform inside the kernel
 * :func:`vq_compressed_bytes`, :func:`vq_validate`, :func:`vq_version`
+* attention between the linears, in :mod:`.attention`: :func:`attn_prompt`,
+  :func:`attn_prompt_weights`, :class:`KV4Cache`, :func:`kv4_append`,
+  :func:`kv4_read`, :func:`kv4_attend`, :func:`kv4_evict`
 
 The C ABI cannot see buffer sizes, so every wrapper checks what it can before
 the call: each tensor is contiguous, on the weight's GPU, of the expected
@@ -33,10 +36,15 @@ from typing import Optional, Sequence
 
 import numpy as np
 
+from .attention import *  # noqa: F401,F403
+from .attention import ATTN_EXPORTS, declare as _declare_attention
+from .attention import __all__ as _attention_all
+
 __all__ = [
     "VQError", "VQWeight", "lib", "LIB_PATH", "vq_version", "vq_validate", "vq_compressed_bytes",
     "vq_unpack_dequant", "vq_gemv", "vq_gemm", "vq_gemm_workspace_size", "vq_gemm_noalloc", "rht_apply",
     "rht_apply_shards", "vq_gemv_rht", "VQ_F32", "VQ_BF16", "VQ_STAGE_SCALES", "VQ_RHT_MAX_SHARDS", "EXPORTS",
+    *_attention_all,
 ]
 
 # VQMM_LIBRARY names another build of the same library (the host-sanitized
@@ -46,7 +54,7 @@ VQ_F32, VQ_BF16 = 0, 1
 MAX_STAGES = 4
 EXPORTS = ("vq_version", "vq_status_string", "vq_validate", "vq_compressed_bytes",
            "vq_unpack_dequant", "vq_gemv", "vq_gemm", "vq_gemm_workspace_size", "vq_gemm_noalloc", "rht_apply",
-           "rht_apply_shards", "vq_gemv_rht")
+           "rht_apply_shards", "vq_gemv_rht") + ATTN_EXPORTS
 VQ_RHT_MAX_SHARDS = 16
 
 _ptr4 = ctypes.c_void_p * MAX_STAGES
@@ -121,6 +129,7 @@ def lib() -> ctypes.CDLL:
         L.rht_apply_shards.restype = ctypes.c_int
         L.vq_gemv_rht.argtypes = [D, P, ctypes.c_int32, ctypes.c_int32, P, ctypes.c_int32, P, P]
         L.vq_gemv_rht.restype = ctypes.c_int
+        _declare_attention(L)
         _LIB = L
     return _LIB
 

@@ -25,7 +25,9 @@ ARCH = "gfx950"
 
 SOURCES = ["vqmm_api.cpp", "k_dequant.hip", "k_rht.hip", "k_gemv.hip", "k_gemv_ladder.hip", "k_gemm.hip",
            "k_gemm_ladder.hip", "k_sparse.hip",
-           "k_gemv_sparse.hip", "k_gemv_l2.hip", "k_gemv_cbs.hip", "k_lowrank.hip"]
+           "k_gemv_sparse.hip", "k_gemv_l2.hip", "k_gemv_cbs.hip", "k_lowrank.hip",
+           "attn_api.cpp", "k_attn_prompt.hip", "k_attn_weights.hip", "k_kv4_store.hip", "k_kv4_attend.hip",
+           "k_kv4_evict.hip"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

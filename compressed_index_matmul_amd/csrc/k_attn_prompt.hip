@@ -1,0 +1,234 @@
+// attn_prompt: softmax(scale Q K^T) V over packed sequences, grouped heads.
+//
+// One pass over the keys with a running maximum and sum.  A workgroup of four
+// waves takes 128 queries of one head, 32 a wave, and walks the keys BN at a
+// time through double-buffered LDS (the next tile's global loads are in flight
+// during the products).  Both products are taken transposed on 32x32x16 MFMA:
+//   S^T = K Q^T   the operand of a query column stays in registers, and a lane
+//                 ends up with half the keys of one query, so maximum and sum
+//                 take one exchange between lane halves;
+//   O^T = V^T P^T the reduction order is free, so the keys a lane holds are
+//                 taken as its eight of the reduction and P never leaves its
+//                 registers; V^T comes out of row-major LDS by the transposing
+//                 reads (4 keys x 16 channels a group of 16 lanes).
+// The reference maximum may lag the running one by 2^8, so most tiles skip the
+// rescale of O.  LDS rows are padded by 16 bytes (K) and 64 bytes (V): the
+// b128 reads of 8 rows, and the transposing reads of 4 rows, then fall on
+// different banks.
+#include "attn_device.h"
+
+namespace vqmm {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 128;  // queries of a workgroup
+constexpr float kSlack = 8.0f;
+
+template <bool F16>
+__device__ __forceinline__ float16_t mfma32(uint4_t a, uint4_t b, float16_t c) {
+  if (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// Four 16-bit values of one column, rows 0..3 of a 4 x 16 block in LDS whose
+// row r, columns 4 j .. 4 j + 3 the lane 4 r + j of the 16 points at.
+__device__ __forceinline__ uint2_t lds_column(const uint16_t *p) {
+  typedef __attribute__((address_space(3))) short4_t lds_short4;
+  return __builtin_bit_cast(uint2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)p));
+}
+
+// BN rows of D channels of one head into registers (rows >= n: zeros), then
+// into LDS.
+template <int D, int BN, int PAD>
+struct Stage {
+  static constexpr int kPieces = BN * (D / 8) / kThreads;
+  uint4_t r[kPieces];
+  __device__ __forceinline__ void load(const uint16_t *base, int64_t ts, int row0, int n) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int id = threadIdx.x + i * kThreads, row = row0 + id / (D / 8), col = id % (D / 8) * 8;
+      r[i] = uint4_t{0, 0, 0, 0};
+      if (row < n) r[i] = *reinterpret_cast<const uint4_t *>(base + row * ts + col);
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t *s) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int id = threadIdx.x + i * kThreads;
+      *reinterpret_cast<uint4_t *>(s + (id / (D / 8)) * (D + PAD) + id % (D / 8) * 8) = r[i];
+    }
+  }
+};
+
+template <int D, int BN, bool F16, bool CAUSAL>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(AttnView a, uint16_t *__restrict__ out,
+                                                                            float *__restrict__ lse, int tiles) {
+  constexpr int KP = 8, VP = 32;  // padding of an LDS row, in elements
+  constexpr int NS = BN / 32, ND = D / 32, NK = D / 16;
+  __shared__ __attribute__((aligned(16))) uint16_t s_k[2][BN * (D + KP)];
+  __shared__ __attribute__((aligned(16))) uint16_t s_v[2][BN * (D + VP)];
+
+  // heads of a group share keys and values: they come next to one another,
+  // key/value heads fastest (workgroups are dealt to the XCDs in turn, so with
+  // 8 of them an XCD's L2 serves one); late tiles, the long ones, first
+  int id = blockIdx.x;
+  const int kvh = id % a.hkv;
+  id /= a.hkv;
+  const int group = a.hq / a.hkv;
+  const int head = kvh * group + id % group;
+  const int vt = tiles - 1 - id / group;
+  int first;
+  const int b = find_tile(a.cu_q, a.nseq, a.tq, kRows, 1, vt, &first);
+  if (b < 0) return;
+  const Rows rq = seq_rows(a.cu_q, b, a.tq), rk = seq_rows(a.cu_k, b, a.tk);
+  const int q0 = (vt - first) * kRows;
+  if (q0 >= rq.n) return;
+  const int off = rk.n - rq.n;  // query i sees keys j <= i + off
+
+  const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int qw = q0 + wave * 32;  // the wave's first query
+  const int qi = qw + col;
+  const int lim = CAUSAL ? min(qi + off, rk.n - 1) : rk.n - 1;  // last key this lane's query sees
+  const int lim_first = CAUSAL ? min(qw + off, rk.n - 1) : rk.n - 1, lim_last = CAUSAL ? min(qw + 31 + off, rk.n - 1) : rk.n - 1;
+  const int seen = CAUSAL ? min(q0 + kRows + off, rk.n) : rk.n;  // keys the workgroup needs
+  const int nt = seen > 0 ? (seen + BN - 1) / BN : 0;
+
+  const uint16_t *kb = a.k + rk.begin * a.k_ts + kvh * a.k_hs;
+  const uint16_t *vb = a.v + rk.begin * a.v_ts + kvh * a.v_hs;
+
+  uint4_t qf[NK];
+  {
+    const uint16_t *qp = a.q + (rq.begin + (int64_t)min(qi, rq.n - 1)) * a.q_ts + head * a.q_hs + 8 * h;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) qf[i] = *reinterpret_cast<const uint4_t *>(qp + 16 * i);
+  }
+  float16_t acc[ND];
+#pragma unroll
+  for (int i = 0; i < ND; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
+  float mref = -INFINITY, lsum = 0.0f;  // in units of scores
+  const float cs = a.scale * kLog2e;
+  const float slack = kSlack / cs;
+
+  Stage<D, BN, KP> sk;
+  Stage<D, BN, VP> sv;
+  if (nt > 0) {
+    sk.load(kb, a.k_ts, 0, seen);
+    sv.load(vb, a.v_ts, 0, seen);
+    sk.store(s_k[0]);
+    sv.store(s_v[0]);
+  }
+  __syncthreads();
+  for (int t = 0; t < nt; ++t) {
+    const int k0 = t * BN;
+    if (t + 1 < nt) {
+      sk.load(kb, a.k_ts, k0 + BN, seen);
+      sv.load(vb, a.v_ts, k0 + BN, seen);
+    }
+    if (k0 <= lim_last) {
+      const uint16_t *ks = s_k[t & 1] + col * (D + KP) + 8 * h;
+      float16_t S[NS];
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[n][r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+          S[n] = mfma32<F16>(*reinterpret_cast<const uint4_t *>(ks + n * 32 * (D + KP) + 16 * i), qf[i], S[n]);
+      }
+      if (k0 + BN - 1 > lim_first) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int key = k0 + 32 * n + 8 * (r / 4) + 4 * h + (r & 3);
+            S[n][r] = key <= lim ? S[n][r] : -INFINITY;
+          }
+      }
+      float top = S[0][0];
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, S[n][r]);
+      top = max_xor32(top);
+      if (__any(top > mref + slack)) {
+        const float mnew = fmaxf(mref, top);
+        const float f = mnew == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((mref - mnew) * cs);
+        lsum *= f;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) acc[i] *= f;
+        mref = mnew;
+      }
+      const float m0 = mref == -INFINITY ? 0.0f : mref * cs;
+      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          S[n][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[n][r], cs, -m0));
+          part[r & 3] += S[n][r];
+        }
+      lsum += (part[0] + part[1]) + (part[2] + part[3]);
+      // V^T: rows 4 h + (i16 / 4), columns 16 (lane / 16 % 2) + 4 (i16 % 4) of each 8-key, 32-channel block
+      const uint16_t *vs = s_v[t & 1] + (4 * h + ((lane & 15) >> 2)) * (D + VP) + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint4_t pf;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pf[i] = pack16<F16>(S[n][8 * x + 2 * i], S[n][8 * x + 2 * i + 1]);
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const uint16_t *vp = vs + (32 * n + 16 * x) * (D + VP) + 32 * d;
+            const uint2_t v0 = lds_column(vp), v1 = lds_column(vp + 8 * (D + VP));
+            acc[d] = mfma32<F16>(uint4_t{v0[0], v0[1], v1[0], v1[1]}, pf, acc[d]);
+          }
+        }
+    }
+    if (t + 1 < nt) {
+      sk.store(s_k[(t + 1) & 1]);
+      sv.store(s_v[(t + 1) & 1]);
+    }
+    __syncthreads();
+  }
+
+  lsum = sum_xor32(lsum);
+  if (qi >= rq.n) return;
+  const float r = lsum == 0.0f ? 0.0f : 1.0f / lsum;
+  const int64_t row = rq.begin + (int64_t)qi;
+  uint16_t *op = out + (row * a.hq + head) * D + 4 * h;
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint2_t w = {pack16<F16>(acc[d][4 * x] * r, acc[d][4 * x + 1] * r),
+                         pack16<F16>(acc[d][4 * x + 2] * r, acc[d][4 * x + 3] * r)};
+      *reinterpret_cast<uint2_t *>(op + 32 * d + 8 * x) = w;
+    }
+  if (lse && h == 0)
+    lse[(int64_t)head * a.tq + row] = (mref == -INFINITY ? 0.0f : mref * a.scale) + __builtin_amdgcn_logf(lsum) * kLn2;
+}
+
+template <int D, int BN, bool F16>
+hipError_t prompt_d(const AttnView &a, uint16_t *out, float *lse, hipStream_t s) {
+  const int tiles = a.tq / kRows + a.nseq;
+  const unsigned grid = (unsigned)((int64_t)tiles * a.hq);
+  if (a.causal) k_attn_prompt<D, BN, F16, true><<<grid, kThreads, 0, s>>>(a, out, lse, tiles);
+  else k_attn_prompt<D, BN, F16, false><<<grid, kThreads, 0, s>>>(a, out, lse, tiles);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_prompt(const AttnView &a, uint16_t *out, float *lse, hipStream_t s) {
+  if (a.d == 64) return a.f16 ? prompt_d<64, 64, true>(a, out, lse, s) : prompt_d<64, 64, false>(a, out, lse, s);
+  if (a.d == 128) return a.f16 ? prompt_d<128, 64, true>(a, out, lse, s) : prompt_d<128, 64, false>(a, out, lse, s);
+  return a.f16 ? prompt_d<256, 32, true>(a, out, lse, s) : prompt_d<256, 32, false>(a, out, lse, s);
+}
+
+}  // namespace vqmm

@@ -1,0 +1,157 @@
+// attn_prompt_weights: the weight each key gathers, the column sums of
+// exp(scale q.k - lse) over a group's heads and a run of queries.
+//
+// A workgroup owns 128 keys of one key/value head, 32 a wave, held in registers
+// as one operand of 32x32x16 MFMA; the queries of the group's heads pass through
+// double-buffered LDS.  S = Q K^T puts a key in a lane's column and 16 queries in
+// its registers, so the sum over queries needs no exchange until the end, and
+// one workgroup sees all the queries of its keys: no atomics, a fixed order.
+#include "attn_device.h"
+
+namespace vqmm {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeys = 128;
+
+template <bool F16>
+__device__ __forceinline__ float16_t mfma32(uint4_t a, uint4_t b, float16_t c) {
+  if (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+template <int D, int BQ, bool F16, bool CAUSAL>
+__global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const float *__restrict__ lse, int last,
+                                                           int accumulate, float *__restrict__ weights) {
+  constexpr int QP = 8, NK = D / 16, NQ = BQ / 32;
+  constexpr int kPieces = BQ * (D / 8) / kThreads;
+  __shared__ __attribute__((aligned(16))) uint16_t s_q[2][BQ * (D + QP)];
+  __shared__ __attribute__((aligned(16))) float s_lse[2][BQ];
+
+  const int kvh = blockIdx.x % a.hkv, vt = blockIdx.x / a.hkv;
+  int first;
+  const int b = find_tile(a.cu_k, a.nseq, a.tk, kKeys, 1, vt, &first);
+  if (b < 0) return;
+  const Rows rq = seq_rows(a.cu_q, b, a.tq), rk = seq_rows(a.cu_k, b, a.tk);
+  const int k0 = (vt - first) * kKeys;
+  if (k0 >= rk.n) return;
+  const int off = rk.n - rq.n;
+  const int group = a.hq / a.hkv;
+
+  const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = k0 + wave * 32, ki = kw + col;
+  uint4_t kf[NK];
+  {
+    const uint16_t *kp = a.k + (rk.begin + (int64_t)min(ki, rk.n - 1)) * a.k_ts + kvh * a.k_hs + 8 * h;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) kf[i] = *reinterpret_cast<const uint4_t *>(kp + 16 * i);
+  }
+
+  // queries from `low` on: the last ones, and of those the ones that see the first key
+  int low = last > 0 ? max(0, rq.n - last) : 0;
+  if (CAUSAL) low = max(low, k0 - off);
+  const int ni = low < rq.n ? (rq.n - low + BQ - 1) / BQ : 0;
+  const int total = ni * group;
+  const float cs = a.scale * kLog2e;
+
+  uint4_t stage[kPieces];
+  float stage_lse = 0.0f;
+  auto fetch = [&](int it) {
+    const int head = kvh * group + it / ni, r0 = low + it % ni * BQ;
+    const uint16_t *qp = a.q + rq.begin * a.q_ts + head * a.q_hs;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int id = threadIdx.x + i * kThreads, row = r0 + id / (D / 8);
+      stage[i] = uint4_t{0, 0, 0, 0};
+      if (row < rq.n) stage[i] = *reinterpret_cast<const uint4_t *>(qp + row * a.q_ts + id % (D / 8) * 8);
+    }
+    if (threadIdx.x < BQ) {
+      // rows past the end, and rows without keys, give exp2(-inf) = 0
+      const int row = r0 + threadIdx.x;
+      const float v = row < rq.n ? lse[(int64_t)head * a.tq + rq.begin + row] : -INFINITY;
+      stage_lse = v == -INFINITY ? INFINITY : v * kLog2e;
+    }
+  };
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int id = threadIdx.x + i * kThreads;
+      *reinterpret_cast<uint4_t *>(&s_q[buf][(id / (D / 8)) * (D + QP) + id % (D / 8) * 8]) = stage[i];
+    }
+    if (threadIdx.x < BQ) s_lse[buf][threadIdx.x] = stage_lse;
+  };
+
+  float sum = 0.0f;
+  if (total > 0) {
+    fetch(0);
+    put(0);
+  }
+  __syncthreads();
+  for (int it = 0; it < total; ++it) {
+    if (it + 1 < total) fetch(it + 1);
+    const int r0 = low + it % ni * BQ;
+    const bool some = !CAUSAL || r0 + BQ - 1 + off >= kw;  // some query of the tile sees some key of the wave
+    if (some) {
+      const bool mask = r0 + BQ > rq.n || (CAUSAL && r0 + off < kw + 31);
+      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float16_t S;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[r] = 0.0f;
+        const uint16_t *qs = &s_q[it & 1][(32 * n + col) * (D + QP) + 8 * h];
+#pragma unroll
+        for (int i = 0; i < NK; ++i) S = mfma32<F16>(*reinterpret_cast<const uint4_t *>(qs + 16 * i), kf[i], S);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int q8 = 32 * n + 8 * x + 4 * h;
+          const float4_t l4 = *reinterpret_cast<const float4_t *>(&s_lse[it & 1][q8]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float p = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * x + i], cs, -l4[i]));
+            if (mask) {
+              const int row = r0 + q8 + i;
+              p = row < rq.n && (!CAUSAL || ki <= row + off) ? p : 0.0f;
+            }
+            part[i] += p;
+          }
+        }
+      }
+      sum += (part[0] + part[1]) + (part[2] + part[3]);
+    }
+    if (it + 1 < total) put((it + 1) & 1);
+    __syncthreads();
+  }
+  sum = sum_xor32(sum);
+  if (h == 0 && ki < rk.n) {
+    float *w = weights + (int64_t)kvh * a.tk + rk.begin + ki;
+    *w = accumulate ? *w + sum : sum;
+  }
+}
+
+template <int D, int BQ, bool F16>
+hipError_t weights_d(const AttnView &a, const float *lse, int last, bool accumulate, float *weights, hipStream_t s) {
+  const unsigned grid = (unsigned)((int64_t)(a.tk / kKeys + a.nseq) * a.hkv);
+  if (a.causal) k_attn_weights<D, BQ, F16, true><<<grid, kThreads, 0, s>>>(a, lse, last, accumulate, weights);
+  else k_attn_weights<D, BQ, F16, false><<<grid, kThreads, 0, s>>>(a, lse, last, accumulate, weights);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_weights(const AttnView &a, const float *lse, int last, bool accumulate, float *weights,
+                               hipStream_t s) {
+  if (a.d == 64)
+    return a.f16 ? weights_d<64, 64, true>(a, lse, last, accumulate, weights, s)
+                 : weights_d<64, 64, false>(a, lse, last, accumulate, weights, s);
+  if (a.d == 128)
+    return a.f16 ? weights_d<128, 64, true>(a, lse, last, accumulate, weights, s)
+                 : weights_d<128, 64, false>(a, lse, last, accumulate, weights, s);
+  return a.f16 ? weights_d<256, 32, true>(a, lse, last, accumulate, weights, s)
+               : weights_d<256, 32, false>(a, lse, last, accumulate, weights, s);
+}
+
+}  // namespace vqmm

@@ -1,0 +1,485 @@
+// kv4_attend: one query a sequence against the 4-bit cache.
+//
+// For every sequence and key/value head the cache is read once, for up to 16
+// query heads of the group at a time (they are the columns of the matrix
+// products).  A wave walks tiles of 32 slots on its own, with the next tile's
+// loads in flight; the four waves of a workgroup and the splits of a long
+// sequence each keep a running maximum and sum and meet at the end, in LDS
+// and in a second launch, in a fixed order.
+//
+// Scores: S^T = K Q^T on 16x16x32 fp16 MFMA, a group of 32 channels a
+// product.  Codes are integers, exact in fp16, so a product is exact up to its
+// fp32 sum; step and minimum come in afterwards, in fp32:
+//   q . k = sum_g s_g (q_g . c_g) + m_g sum(q_g).
+// Output: O^T = V^T P^T.  A lane of the score product holds four slots of one
+// head in each of two 16-slot halves, which is the operand the second product
+// wants when its eight slots of the reduction are those same ones; the values
+// are stored so that a word unpacks to pairs of neighbouring slots, so
+// neither operand crosses lanes.
+//
+// Bound: HBM, 2 (head_dim / 2 + head_dim / 8) bytes a slot and head.
+#include "attn_device.h"
+
+#include <algorithm>
+
+namespace vqmm {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kTile = 32;  // slots a wave takes at a time
+constexpr float kSlack = 8.0f;  // the reference maximum lags by up to 2^8: p <= 256 is in fp16's range
+
+// dword N of the 16 lanes of a row, in all of them.
+template <int N>
+__device__ __forceinline__ uint32_t row_bcast(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + N, 0xF, 0xF, false);
+}
+
+// Eight 4-bit codes of a word as fp16 integers, in the order of the bits 0,
+// 16, 4, 20, 8, 24, 12, 28.  1024 + n has the bits 0x6400 | n in fp16, 1024 +
+// 16 n the bits 0x6400 | n << 4; one packed operation takes the 1024 off.
+__device__ __forceinline__ half2_t code_lo(uint32_t w) {
+  const half2_t bias = {(_Float16)1024.0f, (_Float16)1024.0f};
+  return as_h2((w & 0x000f000fu) | 0x64006400u) - bias;
+}
+__device__ __forceinline__ half2_t code_hi(uint32_t w) {
+  const half2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f}, bias = {(_Float16)64.0f, (_Float16)64.0f};
+  return as_h2((w & 0x00f000f0u) | 0x64006400u) * sixteenth - bias;
+}
+__device__ __forceinline__ half8_t join(half2_t a, half2_t b, half2_t c, half2_t d) {
+  return half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+template <int N>
+struct Words {
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const void *p) {
+    if (N == 2) {
+      const uint2_t v = *static_cast<const uint2_t *>(p);
+      w[0] = v[0], w[1] = v[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const uint4_t v = static_cast<const uint4_t *>(p)[i / 4];
+        w[i] = v[0], w[i + 1] = v[1], w[i + 2] = v[2], w[i + 3] = v[3];
+      }
+    }
+  }
+};
+
+// What a lane loads of one tile.
+template <int D>
+struct Tile {
+  static constexpr int DG = D / 32;
+  static constexpr int SW = DG <= 4 ? 1 : DG / 4;  // dwords of key steps and minima a lane brings in
+  Words<DG> k[2];        // two halves of 16 slots: a lane's DG words of its slot
+  uint32_t ks[2][SW];
+  Words<DG> v[2];        // two quads of slots: a lane's D / 16 channels
+  uint4_t vs[2];
+
+  __device__ __forceinline__ void load(const uint8_t *kb, const uint8_t *vb, const uint16_t *ksb, const uint16_t *vsb,
+                                       int t, int lane) {
+    const int c = lane & 15, h4 = lane >> 4;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      k[u].load(kb + (t * kTile + 16 * u + c) * (D / 2) + h4 * (DG * 4));
+      const uint32_t *sp = reinterpret_cast<const uint32_t *>(ksb + (t * (kTile / 4) + 4 * u + h4) * (DG * 8));
+      if (SW == 1) ks[u][0] = sp[c & (4 * DG - 1)];
+      else {
+        const uint2_t x = reinterpret_cast<const uint2_t *>(sp)[c];
+        ks[u][0] = x[0], ks[u][SW - 1] = x[1];
+      }
+      const int quad = t * (kTile / 4) + 4 * u + h4;
+      v[u].load(vb + quad * (2 * D) + c * (D / 8));
+      vs[u] = *reinterpret_cast<const uint4_t *>(vsb + quad * (DG * 8) + (c * DG / 16) * 8);
+    }
+  }
+};
+
+// One group of the scores of a half: S[i] += s_i D[i] + m_i qsum.
+template <int D, int J>
+__device__ __forceinline__ void add_group(float *S, const Tile<D> &t, int u, half8_t qf, float qsum) {
+  constexpr int SW = Tile<D>::SW;
+  const uint32_t w = t.k[u].w[J];
+  const half8_t kf = join(code_lo(w), code_hi(w), code_lo(w >> 8), code_hi(w >> 8));
+  const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float4_t dot = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf, zero, 0, 0, 0);
+  const half2_t s01 = as_h2(row_bcast<(4 * J + 0) / SW>(t.ks[u][0]));
+  const half2_t s23 = as_h2(row_bcast<(4 * J + 1) / SW>(t.ks[u][SW - 1]));
+  const half2_t m01 = as_h2(row_bcast<(4 * J + 2) / SW>(t.ks[u][0]));
+  const half2_t m23 = as_h2(row_bcast<(4 * J + 3) / SW>(t.ks[u][SW - 1]));
+  S[0] = __builtin_fmaf((float)m01[0], qsum, __builtin_fmaf((float)s01[0], dot[0], S[0]));
+  S[1] = __builtin_fmaf((float)m01[1], qsum, __builtin_fmaf((float)s01[1], dot[1], S[1]));
+  S[2] = __builtin_fmaf((float)m23[0], qsum, __builtin_fmaf((float)s23[0], dot[2], S[2]));
+  S[3] = __builtin_fmaf((float)m23[1], qsum, __builtin_fmaf((float)s23[1], dot[3], S[3]));
+}
+
+template <int D, int J>
+struct AddGroups {
+  static __device__ __forceinline__ void run(float *S, const Tile<D> &t, int u, const half8_t *qf, const float *qsum) {
+    AddGroups<D, J - 1>::run(S, t, u, qf, qsum);
+    add_group<D, J>(S, t, u, qf[J], qsum[J]);
+  }
+};
+template <int D>
+struct AddGroups<D, -1> {
+  static __device__ __forceinline__ void run(float *, const Tile<D> &, int, const half8_t *, const float *) {}
+};
+
+struct AttendArgs {
+  const void *q;
+  int64_t q_ts, q_hs;
+  float scale;
+  int hq;
+  void *out;
+  float *lse;
+  float *part;   // [seq][head][split][D]
+  float *stat;   // [seq][head][split][2]: maximum (log2 domain), sum
+  float *score;  // [seq][head][pitch], log2 domain
+};
+
+template <int D, bool F16, bool WEIGH>
+__global__ __launch_bounds__(kThreads) void k_kv4_attend(KvView c, AttendPlan p, AttendArgs a) {
+  constexpr int DG = D / 32, CH = D / 16;
+  constexpr int kPitch = D + 4;  // floats of a head's row in LDS: 16-byte pieces of 16 rows fall on different banks
+  __shared__ float s_o[kWaves][16][kPitch];
+  __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int id = blockIdx.x;
+  const int split = id % p.splits;
+  id /= p.splits;
+  const int kvh = id % c.hkv;
+  id /= c.hkv;
+  const int ht = id % p.htiles;
+  const int b = id / p.htiles;
+
+  const int len = min(max(c.lens[b], 0), p.len_cap);
+  const int ntiles = (len + kTile - 1) / kTile;
+  const int t_begin = (int)((int64_t)ntiles * split / p.splits), t_end = (int)((int64_t)ntiles * (split + 1) / p.splits);
+  const int heads = min(16, p.group - ht * 16);   // of this workgroup
+  const int head0 = kvh * p.group + ht * 16;
+  const int col = lane & 15, h4 = lane >> 4;
+
+  // the queries, in fp16 after a power-of-two rescale per head, in the order of the unpacked codes
+  half8_t qf[DG];
+  float qsum[DG];
+  float cs;  // scores -> log2 domain
+  {
+    float x[DG][8];
+    float top = 0.0f;
+    const int h = head0 + min(col, heads - 1);
+    const uint16_t *qp = static_cast<const uint16_t *>(a.q) + b * a.q_ts + h * a.q_hs;
+#pragma unroll
+    for (int j = 0; j < DG; ++j) {
+      const uint4_t w = *reinterpret_cast<const uint4_t *>(qp + 8 * (4 * j + h4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (F16) {
+          const half2_t v = as_h2(w[i]);
+          x[j][2 * i] = (float)v[0], x[j][2 * i + 1] = (float)v[1];
+        } else {
+          x[j][2 * i] = bf2f(w[i] & 0xffffu), x[j][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[j][i]));
+    }
+    top = max_xor32(max_xor16(top));
+    // largest |q| to [2^14, 2^15); zero, infinite and very small rows keep a finite factor
+    int e = top > 0.0f && top <= 3.4e38f ? 14 - (int)((__float_as_uint(top) >> 23) - 127) : 0;
+    e = min(max(e, -120), 100);
+    const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+    cs = a.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int j = 0; j < DG; ++j) {
+      float sum = 0.0f;
+      half8_t v;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const _Float16 y = (_Float16)(x[j][i] * up);
+        v[(i & 3) * 2 + (i >> 2)] = y;  // channels 0 4 1 5 2 6 3 7
+        sum += (float)y;
+      }
+      qf[j] = v;
+      qsum[j] = sum_xor32(sum_xor16(sum));
+    }
+  }
+
+  float4_t acc[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) acc[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  float mref = -INFINITY, lsum = 0.0f;
+
+  const int tpp = c.ps / kTile;  // tiles of a page
+  const int64_t code_head = (int64_t)c.ps * (D / 2), scale_head = (int64_t)c.ps * (DG * 2);
+  auto fetch = [&](Tile<D> &t, int tile) {
+    const int pi = tile / tpp;
+    const int64_t page = page_of(c, b, pi);
+    const uint8_t *kb = c.codes + (page * 2 * c.hkv + kvh) * code_head;
+    const uint16_t *sb = c.scales + (page * 2 * c.hkv + kvh) * scale_head;
+    t.load(kb, kb + c.hkv * code_head, sb, sb + c.hkv * scale_head, tile - pi * tpp, lane);
+  };
+
+  Tile<D> cur, next;
+  int tile = t_begin + wave;
+  if (tile < t_end) fetch(next, tile);
+  for (; tile < t_end; tile += kWaves) {
+    cur = next;
+    if (tile + kWaves < t_end) fetch(next, tile + kWaves);
+
+    float S[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) AddGroups<D, DG - 1>::run(S[u], cur, u, qf, qsum);
+
+    const int left = len - tile * kTile;  // slots of the tile that exist
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[u][i] *= cs;
+    if (left < kTile) {  // the last tile: slots past the end count for nothing, whatever they hold
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int in = left - 16 * u - 4 * h4;  // of the lane's four slots
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[u][i] = i < in ? S[u][i] : -INFINITY;
+        const uint32_t m01 = in > 1 ? 0xffffffffu : in > 0 ? 0xffffu : 0u, m23 = in > 3 ? 0xffffffffu : in > 2 ? 0xffffu : 0u;
+        cur.vs[u][0] &= m01, cur.vs[u][1] &= m23, cur.vs[u][2] &= m01, cur.vs[u][3] &= m23;
+      }
+    }
+    if (WEIGH && col < heads) {
+      float *sp = a.score + ((int64_t)b * a.hq + head0 + col) * p.score_pitch + tile * kTile + 4 * h4;
+      *reinterpret_cast<float4_t *>(sp) = float4_t{S[0][0], S[0][1], S[0][2], S[0][3]};
+      *reinterpret_cast<float4_t *>(sp + 16) = float4_t{S[1][0], S[1][1], S[1][2], S[1][3]};
+    }
+
+    float top = fmaxf(fmaxf(fmaxf(S[0][0], S[0][1]), fmaxf(S[0][2], S[0][3])),
+                      fmaxf(fmaxf(S[1][0], S[1][1]), fmaxf(S[1][2], S[1][3])));
+    top = max_xor32(max_xor16(top));
+    if (__any(top > mref + kSlack)) {
+      const float mnew = fmaxf(mref, top);
+      const float f = mnew == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mref - mnew);
+      lsum *= f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) acc[i] *= f;
+      mref = mnew;
+    }
+    const float m0 = mref == -INFINITY ? 0.0f : mref;
+    float P[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        P[u][i] = __builtin_amdgcn_exp2f(S[u][i] - m0);
+        lsum += P[u][i];
+      }
+    const uint4_t pw = {pack16<true>(P[0][0], P[0][1]), pack16<true>(P[0][2], P[0][3]),
+                        pack16<true>(P[1][0], P[1][1]), pack16<true>(P[1][2], P[1][3])};
+    const half8_t pf = __builtin_bit_cast(half8_t, pw);
+
+    half2_t sv[4], mv[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      sv[2 * u] = as_h2(cur.vs[u][0]), sv[2 * u + 1] = as_h2(cur.vs[u][1]);
+      mv[2 * u] = as_h2(cur.vs[u][2]), mv[2 * u + 1] = as_h2(cur.vs[u][3]);
+    }
+#pragma unroll
+    for (int i = 0; i < DG; ++i) {  // two pairs of channels a word: 2 i' = CH channels in all
+      const uint32_t w0 = cur.v[0].w[i], w1 = cur.v[1].w[i];
+      const half8_t lo = join(code_lo(w0) * sv[0] + mv[0], code_lo(w0 >> 8) * sv[1] + mv[1],
+                              code_lo(w1) * sv[2] + mv[2], code_lo(w1 >> 8) * sv[3] + mv[3]);
+      const half8_t hi = join(code_hi(w0) * sv[0] + mv[0], code_hi(w0 >> 8) * sv[1] + mv[1],
+                              code_hi(w1) * sv[2] + mv[2], code_hi(w1 >> 8) * sv[3] + mv[3]);
+      acc[2 * i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, pf, acc[2 * i], 0, 0, 0);
+      acc[2 * i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, pf, acc[2 * i + 1], 0, 0, 0);
+    }
+  }
+
+  // the four waves meet
+  lsum = sum_xor32(sum_xor16(lsum));
+  if (col < heads) {
+    if (h4 == 0) s_m[wave][col] = mref, s_l[wave][col] = lsum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int x = 0; x < CH; x += 4)
+        *reinterpret_cast<float4_t *>(&s_o[wave][col][CH * (4 * h4 + i) + x]) =
+            float4_t{acc[x][i], acc[x + 1][i], acc[x + 2][i], acc[x + 3][i]};
+  }
+  __syncthreads();
+  for (int e = threadIdx.x * 4; e < heads * D; e += kThreads * 4) {
+    const int h = e / D, d = e % D;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_m[w][h]);
+    const float m0 = top == -INFINITY ? 0.0f : top;
+    float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+    float l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(s_m[w][h] - m0);
+      l = __builtin_fmaf(s_l[w][h], f, l);
+      const float4_t ow = *reinterpret_cast<const float4_t *>(&s_o[w][h][d]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(ow[i], f, o[i]);
+    }
+    const int64_t row = (int64_t)b * a.hq + head0 + h;
+    if (p.splits == 1) {
+      const float r = l == 0.0f ? 0.0f : 1.0f / l;
+      const uint2_t w = {pack16<F16>(o[0] * r, o[1] * r), pack16<F16>(o[2] * r, o[3] * r)};
+      *reinterpret_cast<uint2_t *>(static_cast<uint16_t *>(a.out) + row * D + d) = w;
+      if (d == 0 && a.lse) a.lse[row] = (__builtin_amdgcn_logf(l) + m0) * kLn2;
+    } else {
+      *reinterpret_cast<float4_t *>(a.part + (row * p.splits + split) * D + d) = o;
+    }
+    if (d == 0 && (WEIGH || p.splits > 1)) {
+      a.stat[(row * p.splits + split) * 2] = top;
+      a.stat[(row * p.splits + split) * 2 + 1] = l;
+    }
+  }
+}
+
+// Maximum and sum of one head over its splits, by one wave.
+__device__ __forceinline__ void head_stats(const float *stat, int splits, float *top, float *sum) {
+  const int lane = threadIdx.x & 63;
+  float m = -INFINITY;
+  for (int s = lane; s < splits; s += kWave) m = fmaxf(m, stat[2 * s]);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  const float m0 = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  for (int s = lane; s < splits; s += kWave) l = __builtin_fmaf(stat[2 * s + 1], __builtin_amdgcn_exp2f(stat[2 * s] - m0), l);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) l += __shfl_xor(l, o);
+  *top = m0;
+  *sum = l;
+}
+
+constexpr int kWeighSlots = kThreads * 4;  // slots of a workgroup of the weights' part
+
+// The splits meet: the first `out_blocks` workgroups take a head's output
+// each (none when there is one split), the others the weights of a run of
+// slots of one sequence and key/value head.
+template <int D, bool F16>
+__global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, AttendArgs a, int out_blocks, int chunks) {
+  if ((int)blockIdx.x < out_blocks) {
+    constexpr int kSub = kThreads / (D / 4);  // splits summed side by side, four channels a thread
+    __shared__ float s_part[kSub][D];
+    const int64_t row = blockIdx.x;
+    const float *stat = a.stat + row * p.splits * 2;
+    float top, sum;
+    head_stats(stat, p.splits, &top, &sum);
+    const int d = threadIdx.x % (D / 4) * 4, sub = threadIdx.x / (D / 4);
+    float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = sub; s < p.splits; s += kSub) {
+      const float f = __builtin_amdgcn_exp2f(stat[2 * s] - top);
+      const float4_t v = *reinterpret_cast<const float4_t *>(a.part + (row * p.splits + s) * D + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], f, o[i]);
+    }
+    *reinterpret_cast<float4_t *>(&s_part[sub][d]) = o;
+    __syncthreads();
+    const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
+    for (int x = threadIdx.x * 2; x < D; x += kThreads * 2) {
+      float y0 = 0.0f, y1 = 0.0f;
+#pragma unroll
+      for (int s = 0; s < kSub; ++s) y0 += s_part[s][x], y1 += s_part[s][x + 1];
+      *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + row * D + x) = pack16<F16>(y0 * r, y1 * r);
+    }
+    if (threadIdx.x == 0 && a.lse) a.lse[row] = (__builtin_amdgcn_logf(sum) + top) * kLn2;
+    return;
+  }
+  __shared__ float s_top[kWave], s_inv[kWave];
+  int id = blockIdx.x - out_blocks;
+  const int chunk = id % chunks;
+  id /= chunks;
+  const int kvh = id % c.hkv, b = id / c.hkv;
+  const int len = min(max(c.lens[b], 0), p.len_cap);
+  if (chunk * kWeighSlots >= len) return;
+  const int slot = chunk * kWeighSlots + threadIdx.x * 4;
+  float4_t w = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int wave = threadIdx.x >> 6;
+  for (int g0 = 0; g0 < p.group; g0 += kWave) {  // heads of the group, 64 at a time
+    const int ng = min(kWave, p.group - g0);
+    const int64_t row0 = (int64_t)b * a.hq + kvh * p.group + g0;
+    __syncthreads();
+    for (int g = wave; g < ng; g += kWaves) {
+      float top, sum;
+      head_stats(a.stat + (row0 + g) * p.splits * 2, p.splits, &top, &sum);
+      if ((threadIdx.x & 63) == 0) s_top[g] = top, s_inv[g] = sum == 0.0f ? 0.0f : 1.0f / sum;
+    }
+    __syncthreads();
+    if (slot < len)
+      for (int g = 0; g < ng; ++g) {
+        const float4_t x = *reinterpret_cast<const float4_t *>(a.score + (row0 + g) * p.score_pitch + slot);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(x[i] - s_top[g]), s_inv[g], w[i]);
+      }
+  }
+  if (slot >= len) return;
+  const int pi = slot / c.ps;
+  float *wp = c.weights + (page_of(c, b, pi) * c.hkv + kvh) * c.ps + (slot - pi * c.ps);
+  if (slot + 4 <= len) {
+    float4_t old = *reinterpret_cast<const float4_t *>(wp);
+    *reinterpret_cast<float4_t *>(wp) = old + w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (slot + i < len) wp[i] += w[i];
+  }
+}
+
+template <int D, bool F16>
+hipError_t attend_d(const KvView &c, const AttendPlan &p, const AttendArgs &a, bool weigh, hipStream_t s) {
+  const unsigned blocks = (unsigned)((int64_t)c.nseq * c.hkv * p.htiles * p.splits);
+  if (weigh) k_kv4_attend<D, F16, true><<<blocks, kThreads, 0, s>>>(c, p, a);
+  else k_kv4_attend<D, F16, false><<<blocks, kThreads, 0, s>>>(c, p, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (p.splits == 1 && !weigh)) return e;
+  const int out_blocks = p.splits > 1 ? c.nseq * a.hq : 0;
+  const int chunks = weigh ? (p.len_cap + kWeighSlots - 1) / kWeighSlots : 0;
+  const int64_t grid = out_blocks + (int64_t)chunks * c.nseq * c.hkv;
+  if (grid == 0) return hipSuccess;
+  if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+  k_kv4_join<D, F16><<<(unsigned)grid, kThreads, 0, s>>>(c, p, a, out_blocks, chunks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add_weights) {
+  AttendPlan p{};
+  p.group = n_q_heads / c.hkv;
+  p.htiles = (p.group + 15) / 16;
+  p.len_cap = (int)std::min<int64_t>(max_len, (int64_t)c.mp * c.ps);
+  // enough pieces to give every CU four workgroups, none shorter than the
+  // 128 slots that its waves take in one round
+  const int64_t work = (int64_t)c.nseq * c.hkv * p.htiles;
+  const int64_t want = (4 * 256 + work - 1) / work, most = ((int64_t)p.len_cap + kWaves * kTile - 1) / (kWaves * kTile);
+  p.splits = (int)std::max<int64_t>(1, std::min(want, most));
+  p.score_pitch = (p.len_cap + kTile - 1) / kTile * kTile;
+  const size_t rows = (size_t)c.nseq * n_q_heads;
+  auto round = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  p.part_off = 0;
+  p.stat_off = p.splits > 1 ? round(rows * p.splits * c.d * 4) : 0;
+  p.score_off = p.stat_off + (p.splits > 1 || add_weights ? round(rows * p.splits * 8) : 0);
+  p.bytes = p.score_off + (add_weights ? round(rows * p.score_pitch * 4) : 0);
+  return p;
+}
+
+hipError_t launch_kv4_attend(const KvView &c, const AttendPlan &p, const void *q, int64_t q_ts, int64_t q_hs, bool f16,
+                             int n_q_heads, float scale, bool add_weights, void *out, float *lse, void *ws,
+                             hipStream_t s) {
+  char *w = static_cast<char *>(ws);
+  AttendArgs a{q, q_ts, q_hs, scale, n_q_heads, out, lse, reinterpret_cast<float *>(w + p.part_off),
+               reinterpret_cast<float *>(w + p.stat_off), reinterpret_cast<float *>(w + p.score_off)};
+  if (c.d == 64) return f16 ? attend_d<64, true>(c, p, a, add_weights, s) : attend_d<64, false>(c, p, a, add_weights, s);
+  if (c.d == 128)
+    return f16 ? attend_d<128, true>(c, p, a, add_weights, s) : attend_d<128, false>(c, p, a, add_weights, s);
+  return f16 ? attend_d<256, true>(c, p, a, add_weights, s) : attend_d<256, false>(c, p, a, add_weights, s);
+}
+
+}  // namespace vqmm

@@ -89,5 +89,57 @@ hipError_t launch_lowrank_tokens(const WView &w, const void *x, int xt, int batc
 size_t lowrank_workspace_bytes(const WView &w, int m);
 hipError_t launch_lowrank_gemm(const WView &w, const uint16_t *x, int m, float *y, float *t, hipStream_t s);
 
+// ---- attention (attn_api.cpp, k_attn_*.hip, k_kv4_*.hip) ----
+
+// A validated attn_batch with its tensors.
+struct AttnView {
+  int hq, hkv, d, nseq, tq, tk;
+  bool causal, f16;
+  float scale;
+  const int32_t *cu_q, *cu_k;
+  const uint16_t *q, *k, *v;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;  // strides in elements
+};
+hipError_t launch_attn_prompt(const AttnView &a, uint16_t *out, float *lse, hipStream_t s);
+hipError_t launch_attn_weights(const AttnView &a, const float *lse, int last, bool accumulate, float *weights,
+                               hipStream_t s);
+
+// A validated cache with its sequences.
+struct KvView {
+  int np, ps, hkv, d;
+  uint8_t *codes;
+  uint16_t *scales;
+  float *weights;
+  int32_t *pos;
+  int nseq, mp;              // sequences, pages per row of the block table
+  const int32_t *table;
+  const int32_t *lens;
+};
+hipError_t launch_kv4_append(const KvView &c, const void *k, const void *v, int64_t k_ts, int64_t k_hs, int64_t v_ts,
+                             int64_t v_hs, int dtype, int total, const int32_t *cu, const int32_t *pos,
+                             const float *weights, hipStream_t s);
+hipError_t launch_kv4_read(const KvView &c, const int32_t *cu, int total, int dtype, void *k_out, void *v_out,
+                           hipStream_t s);
+// How kv4_attend cuts its work and lays out its workspace: a function of
+// sizes only, the same on the host's sizing call and at the launch.
+struct AttendPlan {
+  int group;        // query heads per key/value head
+  int htiles;       // 16-head tiles of a group
+  int splits;       // pieces of the slots of one sequence and head
+  int len_cap;      // lengths are clamped to this
+  int score_pitch;  // floats per head of stored scores (add_weights)
+  size_t part_off, stat_off, score_off, bytes;
+};
+AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add_weights);
+hipError_t launch_kv4_attend(const KvView &c, const AttendPlan &p, const void *q, int64_t q_ts, int64_t q_hs, bool f16,
+                             int n_q_heads, float scale, bool add_weights, void *out, float *lse, void *ws,
+                             hipStream_t s);
+struct EvictPlan {
+  int len_cap, max_moves;
+  size_t key_off, move_off, count_off, bytes;
+};
+EvictPlan kv4_evict_plan(const KvView &c, int keep, int max_len);
+hipError_t launch_kv4_evict(const KvView &c, const EvictPlan &p, const int32_t *next_pos, int keep, int recent,
+                            void *ws, hipStream_t s);
 
 }  // namespace vqmm

@@ -42,7 +42,7 @@
 extern "C" {
 #endif
 
-#define VQMM_VERSION 5
+#define VQMM_VERSION 6
 #define VQ_MAX_STAGES 4
 
 /* vq_weight.flags: stage_scale[] holds one residual scale per stage. */
@@ -63,8 +63,9 @@ typedef enum vq_status {
   VQ_ERR_WORKSPACE = -8    /* the caller's workspace is smaller than vq_gemm_workspace_size */
 } vq_status;
 
-/* Element types of activations. */
-typedef enum vq_dtype { VQ_F32 = 0, VQ_BF16 = 1 } vq_dtype;
+/* Element types of activations.  VQ_F16 is taken by the attention entry
+ * points only; the products and transforms take VQ_F32 and VQ_BF16. */
+typedef enum vq_dtype { VQ_F32 = 0, VQ_BF16 = 1, VQ_F16 = 2 } vq_dtype;
 
 /*
  * Descriptor of one compressed weight (array pointers are device memory).
@@ -377,6 +378,193 @@ int rht_apply_shards(const void *x, int32_t x_dtype, int32_t batch, int32_t n, i
  */
 int vq_gemv_rht(const vq_weight *w, const void *x, int32_t x_dtype, int32_t batch, const int8_t *signs,
                 int32_t max_block, float *y, void *stream);
+
+/* ======================================================================
+ * Attention: what a decoder layer needs between its compressed linears.
+ * Packed prompts, a key/value cache held in 4 bits, single tokens against
+ * that cache, and eviction from it by accumulated attention weight.
+ *
+ * The conventions above hold (device pointers, host-side validation before
+ * any HIP call, no allocation, fixed reduction order, no atomics that could
+ * change a result).  Lengths, tables and slots are device data the host
+ * cannot check; the kernels clamp them (sequence bounds to the packed rows,
+ * page numbers to the pool, lengths to the block table's capacity), so
+ * inconsistent data gives wrong values, never an access outside the arrays.
+ *
+ * Heads are grouped: query head h reads key/value head h / (n_q_heads /
+ * n_kv_heads).  head_dim is 64, 128 or 256.
+ * ====================================================================== */
+
+/* Rows of heads: element (token, head, channel) of a tensor is
+ * data[token * token_stride + head * head_stride + channel], strides in
+ * elements.  data is 16-byte aligned and both strides are positive multiples
+ * of 8 (VQ_ERR_ALIGN, VQ_ERR_SHAPE otherwise), token_stride below 2^22: q, k
+ * and v may be slices of one fused row. */
+typedef struct attn_heads {
+  const void *data;
+  int64_t token_stride;
+  int64_t head_stride;
+} attn_heads;
+
+/* A batch of packed sequences.  Sequence b has the query rows cu_q[b] ..
+ * cu_q[b+1]-1 and the key rows cu_k[b] .. cu_k[b+1]-1 (int32 [n_seqs + 1] on
+ * the device, non-decreasing from 0, the last one total_q / total_k).
+ * causal: with Lq queries and Lk keys, query i sees keys j <= i + Lk - Lq
+ * (the last query sees the last key: a chunk against its prefix); otherwise
+ * every key of its sequence. */
+typedef struct attn_batch {
+  int32_t dtype;      /* VQ_BF16 or VQ_F16: q, k, v and out */
+  int32_t n_q_heads;  /* a multiple of n_kv_heads */
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t n_seqs;
+  int32_t total_q;    /* query rows, >= 0 */
+  int32_t total_k;    /* key rows, >= 0 */
+  int32_t causal;     /* 0 or 1 */
+  float scale;        /* finite, > 0 (VQ_ERR_VALUE otherwise) */
+  int32_t reserved;   /* set to 0 */
+  const int32_t *cu_q;
+  const int32_t *cu_k;
+} attn_batch;
+
+/*
+ * Attention over packed prompts:
+ *   s_ij = scale q_i . k_j over the keys j that query i sees,
+ *   lse_i = log sum_j exp s_ij,   out_i = sum_j exp(s_ij - lse_i) v_j.
+ *   out : [total_q][n_q_heads][head_dim] of the batch's dtype
+ *   lse : float [n_q_heads][total_q], or NULL
+ * A query that sees no key gives out = 0 and lse = -inf.  Scores, the running
+ * maximum and sum and the output sum are fp32; the probabilities enter the
+ * second product rounded to the 16-bit type of v.  Key rows outside a
+ * sequence never reach its result, whatever they hold.
+ */
+int attn_prompt(const attn_batch *b, const attn_heads *q, const attn_heads *k, const attn_heads *v, void *out,
+                float *lse, void *stream);
+
+/*
+ * The attention weight each key gathers from a prompt's queries:
+ *   weights[h][j] = sum over the query heads of group h and over the queries
+ *   i that see j, of the last `last` of j's sequence (0: all), of
+ *   exp(s_ij - lse_i).
+ *   lse        : float [n_q_heads][total_q], as attn_prompt gives it
+ *   accumulate : 0 writes weights, 1 adds to them
+ *   weights    : float [n_kv_heads][total_k]
+ * fp32 throughout but for the 16-bit q and k.
+ */
+int attn_prompt_weights(const attn_batch *b, const attn_heads *q, const attn_heads *k, const float *lse, int32_t last,
+                        int32_t accumulate, float *weights, void *stream);
+
+/* ----------------------------------------------------------------------
+ * The 4-bit cache.  A pool of pages of page_size slots; a slot holds one
+ * token's key and value of one key/value head.  Values are held in groups
+ * of 32 channels: m = f16(min), s = f16((max - min) * (1/15)), code =
+ * clamp(rint((x - m) * (1/s)), 0, 15), each step one fp32 operation (1/s and
+ * 1/15 rounded to fp32; s = 0 gives code 0), and stand for s * code + m:
+ * 5 bits a value.  Inputs beyond +-32768 saturate; a NaN makes its group NaN.
+ *
+ *   codes   uint8 [n_pages][2][n_kv_heads][page_size * head_dim / 2], keys
+ *           (0) then values (1).  With DG = head_dim / 32:
+ *           keys: head_dim / 2 bytes a slot; 32-bit word a * DG + j (a < 4)
+ *           holds the octet of channels 8 (4 j + a) .. + 7, channel i of it
+ *           in bits 4 i .. 4 i + 3: a lane of the decode kernel reads its
+ *           DG matrix operands in one piece;
+ *           values: 2 head_dim bytes per 4 slots; byte (c / 2) * 4 + p holds
+ *           channels c (low bits) and c + 1 (c even) of slot {0, 2, 1, 3}[p]
+ *           of the four: a word unpacks to pairs of neighbouring slots.
+ *   scales  fp16 [n_pages][2][n_kv_heads][page_size / 4][DG][8]: s of the
+ *           four slots, then m of the four.
+ *   weights float [n_pages][n_kv_heads][page_size]: accumulated weight
+ *   pos     int32 [n_pages][n_kv_heads][page_size]: the token's position
+ * ---------------------------------------------------------------------- */
+typedef struct kv4_cache {
+  int32_t n_pages;
+  int32_t page_size;  /* slots, a multiple of 32, at most 1024 */
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  uint8_t *codes;
+  uint16_t *scales;
+  float *weights;
+  int32_t *pos;
+} kv4_cache;
+
+/* Sequences of a cache: slot i of sequence b is slot i % page_size of page
+ * block_table[b][i / page_size].  max_pages * page_size is below 2^31. */
+typedef struct kv4_seqs {
+  int32_t n_seqs;
+  int32_t max_pages;
+  const int32_t *block_table; /* int32 [n_seqs][max_pages] */
+  const int32_t *lens;        /* int32 [n_seqs]: see each call */
+} kv4_seqs;
+
+/*
+ * Store packed keys and values: row cu[b] + i goes to slot lens[b] + i of
+ * sequence b (lens: the length before the call, which the caller then raises;
+ * NULL means 0), for each key/value head.  Rows past the block table's
+ * capacity are dropped.
+ *   k, v    : [total][n_kv_heads][head_dim] of `dtype`, VQ_F32, VQ_BF16 or
+ *             VQ_F16 (VQ_F32 is what the compressed products give)
+ *   cu      : int32 [n_seqs + 1] on the device
+ *   pos     : int32 [n_seqs], the position of each sequence's first row, or
+ *             NULL (its slot number)
+ *   weights : float [n_kv_heads][total] stored as the slots' accumulated
+ *             weight (attn_prompt_weights), or NULL (0)
+ */
+int kv4_append(const kv4_cache *c, const kv4_seqs *s, const attn_heads *k, const attn_heads *v, int32_t dtype,
+               int32_t total, const int32_t *cu, const int32_t *pos, const float *weights, void *stream);
+
+/*
+ * Read slots lens[b] + i (lens NULL: from 0) back into packed rows cu[b] + i
+ * of k_out and v_out, [total][n_kv_heads][head_dim] of `dtype`, each value
+ * rounded once: the keys and values of a prefix, for attn_prompt.  Rows past
+ * the block table's capacity are zeroed.
+ */
+int kv4_read(const kv4_cache *c, const kv4_seqs *s, const int32_t *cu, int32_t total, int32_t dtype, void *k_out,
+             void *v_out, void *stream);
+
+/*
+ * One query a sequence over the sequence's first lens[b] slots, straight from
+ * the 4-bit cache:
+ *   q       : [n_seqs][n_q_heads][head_dim] of dtype, VQ_BF16 or VQ_F16
+ *   max_len : the host's bound on lens; a longer length counts as max_len
+ *             (and every length as at most max_pages * page_size)
+ *   add_weights : 1 adds each slot's weight, summed over the heads of its
+ *             group, to the cache's weights (pages shared between sequences
+ *             must not be added to); 0 leaves them
+ *   out     : [n_seqs][n_q_heads][head_dim] of dtype
+ *   lse     : float [n_seqs][n_q_heads], or NULL
+ *   workspace : 16-byte aligned, at least kv4_attend_workspace_size bytes
+ * An empty sequence gives out = 0, lse = -inf.  Scores are exact sums of
+ * 16-bit queries and integer codes, scaled and summed in fp32 (queries are
+ * held in fp16 after a power-of-two rescale per head, exact for every value
+ * within 2^28 of the head's largest); values are rounded to fp16 (relative
+ * error 2^-11) and so are the probabilities, both summed in fp32.
+ */
+int kv4_attend(const kv4_cache *c, const kv4_seqs *s, const attn_heads *q, int32_t dtype, int32_t n_q_heads,
+               float scale, int32_t max_len, int32_t add_weights, void *out, float *lse, void *workspace,
+               size_t ws_bytes, void *stream);
+
+/* Bytes of workspace kv4_attend needs; 0 for sizes it refuses.  Host only. */
+size_t kv4_attend_workspace_size(const kv4_cache *c, int32_t n_seqs, int32_t n_q_heads, int32_t max_len,
+                                 int32_t add_weights);
+
+/*
+ * Cut every sequence with more than `keep` slots down to keep slots, for each
+ * key/value head on its own.  Kept are the slots with pos >= next_pos[b] -
+ * recent, then those of the largest accumulated weight (NaN counts as the
+ * lowest; ties go to the lowest slot).  Kept slots at or above keep then move into the
+ * free ones below it, the lowest to the lowest, with their weight and
+ * position; everything else stays where it is.  The caller then lowers the
+ * lengths to min(lens, keep).  Attention does not depend on the slots' order.
+ *   next_pos : int32 [n_seqs], the position of the next token
+ *   keep     : >= 1;  recent : 0..keep
+ *   max_len  : as for kv4_attend
+ *   workspace : 16-byte aligned, at least kv4_evict_workspace_size bytes
+ */
+int kv4_evict(const kv4_cache *c, const kv4_seqs *s, const int32_t *next_pos, int32_t keep, int32_t recent,
+              int32_t max_len, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace kv4_evict needs; 0 for sizes it refuses.  Host only. */
+size_t kv4_evict_workspace_size(const kv4_cache *c, int32_t n_seqs, int32_t keep, int32_t max_len);
 
 #ifdef __cplusplus
 }
