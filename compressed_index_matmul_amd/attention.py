@@ -27,6 +27,8 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
+import torch
+
 __all__ = ["VQ_F16", "KV4Cache", "attn_prompt", "attn_prompt_weights", "kv4_append", "kv4_read", "kv4_attend",
            "kv4_attend_workspace_size", "kv4_evict", "kv4_evict_workspace_size"]
 
@@ -86,41 +88,48 @@ def _pkg():
     return m
 
 
+_FN = {}
+
+
+def _fn(name):
+    f = _FN.get(name)
+    if f is None:
+        f = _FN[name] = getattr(_pkg().lib(), name)
+    return f
+
+
 def _call(name, dev, stream, own, *args):
     """One library call on `stream` with `dev` current; `own`: tensors this
     call allocated, kept from reuse until the stream is done with them."""
-    import torch
-    pkg = _pkg()
-    fn = getattr(pkg.lib(), name)
+    fn = _FN.get(name) or _fn(name)
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
         for t in own:
-            if t is not None:
-                t.record_stream(st)
-    if torch.cuda.current_device() == dev.index:
+            t.record_stream(st)
+    if torch._C._cuda_getDevice() == dev.index:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
             status = fn(*args, handle)
     if status != 0:
-        raise pkg.VQError(status, name)
+        raise _pkg().VQError(status, name)
+
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: VQ_F16}
 
 
 def _half(t, name: str) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return 1
-    if t.dtype == torch.float16:
-        return VQ_F16
-    raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    v = _TYPES.get(t.dtype, 0)
+    if not v:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return v
 
 
 def _any_type(dtype, name: str) -> int:
-    import torch
-    v = {torch.float32: 0, torch.bfloat16: 1, torch.float16: VQ_F16}.get(dtype)
+    v = _TYPES.get(dtype)
     if v is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
     return v
@@ -128,12 +137,11 @@ def _any_type(dtype, name: str) -> int:
 
 def _heads(t, name: str, dev=None) -> AttnHeads:
     """[tokens, heads, head_dim] on the GPU `dev` (any, when None)."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dim() != 3:
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected [tokens, heads, head_dim]")
-    if t.device.type != "cuda" or (dev is not None and t.device != dev):
+    if not t.is_cuda or (dev is not None and t.device != dev):
         raise ValueError(f"{name} is on {t.device}; it must be on {dev or 'a GPU'}")
     n, h, d = t.shape
     ts, hs, cs = t.stride()
@@ -143,32 +151,35 @@ def _heads(t, name: str, dev=None) -> AttnHeads:
         ts = h * d  # the stride of a single row has no meaning
     if h <= 1:
         hs = d
-    if ts < 8 or hs < 8 or ts % 8 or hs % 8 or ts >= 1 << 22:
+    if ts < 8 or hs < 8 or (ts | hs) & 7 or ts >= 1 << 22:
         raise ValueError(f"{name}: strides {t.stride()} must be positive multiples of 8, between tokens below 2^22")
     p = t.data_ptr()
-    if p % 16:
+    if p & 15:
         raise ValueError(f"{name} must start at a 16-byte boundary")
     return AttnHeads(p, ts, hs)
 
 
-def _ints(t, shape, dev, name: str) -> int:
-    """Address of a contiguous int32 tensor of the shape."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != torch.int32 or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int32 {shape} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
 def _array(t, shape, dtype, dev, name: str) -> int:
-    import torch
+    """Address of a contiguous tensor of the shape and type on the GPU `dev`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype or t.device != dev or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on "
                          f"{t.device}")
     return t.data_ptr()
+
+
+def _ints(t, shape, dev, name: str) -> int:
+    return _array(t, shape, torch.int32, dev, name)
+
+
+def _output(out, like, dev, own):
+    """`out`, checked, or a new tensor of `like`'s shape and type; its address."""
+    if out is not None:
+        return out, _array(out, like.shape, like.dtype, dev, "out")
+    out = torch.empty(like.shape, dtype=like.dtype, device=dev)
+    own.append(out)
+    return out, out.data_ptr()
 
 
 def _batch(q, k, cu_q, cu_k, scale, causal):
@@ -203,7 +214,6 @@ def attn_prompt(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, causal:
     causal: query i of Lq sees keys j <= i + Lk - Lq.  A query that sees no key
     gives zeros (lse -inf).  Returns out [Tq, Hq, D], with return_lse also the
     scores' log sum of exponentials, float32 [Hq, Tq]."""
-    import torch
     hq_ = _heads(q, "q")
     dev = q.device
     hk, hv = _heads(k, "k", dev), _heads(v, "v", dev)
@@ -211,10 +221,7 @@ def attn_prompt(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, causal:
     if v.dtype != q.dtype or v.shape != k.shape:
         raise ValueError(f"v must be {q.dtype} {tuple(k.shape)}, got {v.dtype} {tuple(v.shape)}")
     own = []
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        own.append(out)
-    po = _array(out, q.shape, q.dtype, dev, "out")
+    out, po = _output(out, q, dev, own)
     lse = None
     if return_lse:
         lse = torch.empty((b.n_q_heads, b.total_q), dtype=torch.float32, device=dev)
@@ -231,7 +238,6 @@ def attn_prompt_weights(q, k, lse, cu_q, cu_k=None, scale: Optional[float] = Non
     the heads of its group and over the last `last` queries of its sequence (0:
     all).  q, k, cu_q, cu_k, scale, causal and lse as attn_prompt takes and
     gives them; accumulate adds to `out` instead of writing it."""
-    import torch
     hq_ = _heads(q, "q")
     dev = q.device
     hk = _heads(k, "k", dev)
@@ -262,7 +268,6 @@ class KV4Cache:
     is the C header's."""
 
     def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda"):
-        import torch
         if n_pages < 1 or n_kv_heads < 1 or page_size < 32 or page_size > 1024 or page_size % 32:
             raise ValueError(f"invalid cache: {n_pages} pages of {page_size} slots, {n_kv_heads} heads (page_size is a "
                              "multiple of 32 up to 1024)")
@@ -282,7 +287,6 @@ class KV4Cache:
         return self
 
     def _set(self, codes, scales, weights, pos):
-        import torch
         if weights.dim() != 3 or scales.dim() != 6:
             raise ValueError("weights must be [pages, heads, slots] and scales [pages, 2, heads, slots / 4, groups, 8]")
         n, h, ps = weights.shape
@@ -306,7 +310,6 @@ class KV4Cache:
 
 
 def _seqs(cache: KV4Cache, block_table, lens, name: str) -> KV4Seqs:
-    import torch
     dev = cache.device
     if dev.type != "cuda":
         raise ValueError(f"the cache is on {dev}; the kernels need it on a GPU")
@@ -327,7 +330,6 @@ def kv4_append(cache: KV4Cache, k, v, cu, block_table, start=None, pos=None, wei
     int32 [sequences]; pos int32 [sequences], the position of each sequence's
     first row (None: its slot); weights float32 [Hkv, T], the slots' accumulated
     weight so far (None: 0).  The caller raises the lengths."""
-    import torch
     s = _seqs(cache, block_table, start, "start")
     dev = cache.device
     hk, hv = _heads(k, "k", dev), _heads(v, "v", dev)
@@ -348,7 +350,6 @@ def kv4_read(cache: KV4Cache, cu, block_table, total: int, start=None, dtype=Non
     """Slots start[b] + i of every sequence as packed rows: (k, v), each
     [total, Hkv, D] of dtype (bfloat16 by default).  total is cu's last entry
     (rows beyond cu are left as allocated)."""
-    import torch
     s = _seqs(cache, block_table, start, "start")
     dev = cache.device
     dtype = torch.bfloat16 if dtype is None else dtype
@@ -365,11 +366,10 @@ def kv4_read(cache: KV4Cache, cu, block_table, total: int, start=None, dtype=Non
 
 def kv4_attend_workspace_size(cache: KV4Cache, n_seqs: int, n_q_heads: int, max_len: int, add_weights: bool = False) -> int:
     """Bytes of workspace kv4_attend needs."""
-    return int(_pkg().lib().kv4_attend_workspace_size(cache.desc, n_seqs, n_q_heads, max_len, int(bool(add_weights))))
+    return _fn("kv4_attend_workspace_size")(cache.desc, n_seqs, n_q_heads, max_len, int(bool(add_weights)))
 
 
 def _workspace(workspace, need: int, dev, own):
-    import torch
     if workspace is None:
         if not need:
             return None, 0
@@ -392,7 +392,6 @@ def kv4_attend(q, cache: KV4Cache, block_table, lens, scale: Optional[float] = N
     kv4_attend_workspace_size bytes (None allocates).  Returns out, with
     return_lse also float32 [sequences, Hq].  An empty sequence gives zeros
     and -inf."""
-    import torch
     s = _seqs(cache, block_table, lens, "lens")
     if lens is None:
         raise ValueError("kv4_attend needs lens")
@@ -408,10 +407,7 @@ def kv4_attend(q, cache: KV4Cache, block_table, lens, scale: Optional[float] = N
         raise ValueError(f"max_len must not be negative, got {max_len}")
     max_len = min(max_len, capacity)
     own = []
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        own.append(out)
-    po = _array(out, q.shape, q.dtype, dev, "out")
+    out, po = _output(out, q, dev, own)
     lse = None
     if return_lse:
         lse = torch.empty((n, hq), dtype=torch.float32, device=dev)
@@ -426,7 +422,7 @@ def kv4_attend(q, cache: KV4Cache, block_table, lens, scale: Optional[float] = N
 
 def kv4_evict_workspace_size(cache: KV4Cache, n_seqs: int, keep: int, max_len: int) -> int:
     """Bytes of workspace kv4_evict needs."""
-    return int(_pkg().lib().kv4_evict_workspace_size(cache.desc, n_seqs, keep, max_len))
+    return _fn("kv4_evict_workspace_size")(cache.desc, n_seqs, keep, max_len)
 
 
 def kv4_evict(cache: KV4Cache, block_table, lens, next_pos, keep: int, recent: int, max_len: Optional[int] = None,
