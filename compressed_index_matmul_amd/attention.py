@@ -62,7 +62,8 @@ class KV4Seqs(ctypes.Structure):
     _fields_ = [("n_seqs", _I32), ("max_pages", _I32), ("block_table", _P), ("lens", _P)]
 
 
-ATTN_EXPORTS = ("attn_prompt", "attn_prompt_weights", "kv4_append", "kv4_read", "kv4_attend",
+ATTN_EXPORTS = ("attn_prompt", "attn_prompt_workspace_size", "attn_prompt_weights",
+                "attn_prompt_weights_workspace_size", "kv4_append", "kv4_read", "kv4_attend",
                 "kv4_attend_workspace_size", "kv4_evict", "kv4_evict_workspace_size")
 
 
@@ -71,8 +72,10 @@ def declare(L) -> None:
     H, B, C, S = (ctypes.POINTER(t) for t in (AttnHeads, AttnBatch, KV4CacheDesc, KV4Seqs))
     z = ctypes.c_size_t
     for name, res, args in (
-            ("attn_prompt", ctypes.c_int, [B, H, H, H, _P, _P, _P]),
-            ("attn_prompt_weights", ctypes.c_int, [B, H, H, _P, _I32, _I32, _P, _P]),
+            ("attn_prompt", ctypes.c_int, [B, H, H, H, _P, _P, _P, z, _P]),
+            ("attn_prompt_workspace_size", z, [B]),
+            ("attn_prompt_weights", ctypes.c_int, [B, H, H, _P, _I32, _I32, _P, _P, z, _P]),
+            ("attn_prompt_weights_workspace_size", z, [B, _I32]),
             ("kv4_append", ctypes.c_int, [C, S, H, H, _I32, _I32, _P, _P, _P, _P]),
             ("kv4_read", ctypes.c_int, [C, S, _P, _I32, _I32, _P, _P, _P]),
             ("kv4_attend", ctypes.c_int, [C, S, H, _I32, _I32, ctypes.c_float, _I32, _I32, _P, _P, _P, z, _P]),
@@ -205,15 +208,16 @@ def _batch(q, k, cu_q, cu_k, scale, causal):
 
 
 def attn_prompt(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, causal: bool = True, out=None,
-                return_lse: bool = False, stream=None):
+                return_lse: bool = False, workspace=None, stream=None):
     """softmax(scale q k^T) v over packed sequences.
 
     q [Tq, Hq, D], k and v [Tk, Hkv, D], bfloat16 or float16, Hq a multiple of
     Hkv, D 64, 128 or 256; cu_q (and cu_k, where the keys are packed
     differently: a chunk against its prefix) int32 [sequences + 1] offsets.
     causal: query i of Lq sees keys j <= i + Lk - Lq.  A query that sees no key
-    gives zeros (lse -inf).  Returns out [Tq, Hq, D], with return_lse also the
-    scores' log sum of exponentials, float32 [Hq, Tq]."""
+    gives zeros (lse -inf).  workspace: a device tensor (None allocates what
+    the call needs).  Returns out [Tq, Hq, D], with return_lse also the scores'
+    log sum of exponentials, float32 [Hq, Tq]."""
     hq_ = _heads(q, "q")
     dev = q.device
     hk, hv = _heads(k, "k", dev), _heads(v, "v", dev)
@@ -228,16 +232,18 @@ def attn_prompt(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, causal:
         own.append(lse)
     if b.n_seqs == 0 and b.total_q:
         raise ValueError("rows without a sequence")
-    _call("attn_prompt", dev, stream, own, b, hq_, hk, hv, po, None if lse is None else lse.data_ptr())
+    pw, wb = _workspace(workspace, _fn("attn_prompt_workspace_size")(b) if workspace is None else 0, dev, own)
+    _call("attn_prompt", dev, stream, own, b, hq_, hk, hv, po, None if lse is None else lse.data_ptr(), pw, wb)
     return (out, lse) if return_lse else out
 
 
 def attn_prompt_weights(q, k, lse, cu_q, cu_k=None, scale: Optional[float] = None, causal: bool = True, last: int = 0,
-                        out=None, accumulate: bool = False, stream=None):
+                        out=None, accumulate: bool = False, workspace=None, stream=None):
     """The attention weight every key gathers: float32 [Hkv, Tk], summed over
     the heads of its group and over the last `last` queries of its sequence (0:
     all).  q, k, cu_q, cu_k, scale, causal and lse as attn_prompt takes and
-    gives them; accumulate adds to `out` instead of writing it."""
+    gives them; accumulate adds to `out` instead of writing it; workspace as
+    for attn_prompt."""
     hq_ = _heads(q, "q")
     dev = q.device
     hk = _heads(k, "k", dev)
@@ -256,7 +262,9 @@ def attn_prompt_weights(q, k, lse, cu_q, cu_k=None, scale: Optional[float] = Non
     po = _array(out, shape, torch.float32, dev, "out")
     if b.n_seqs == 0 and b.total_k:
         raise ValueError("rows without a sequence")
-    _call("attn_prompt_weights", dev, stream, own, b, hq_, hk, pl, min(last, 2**31 - 1), int(bool(accumulate)), po)
+    last = min(last, 2**31 - 1)
+    pw, wb = _workspace(workspace, _fn("attn_prompt_weights_workspace_size")(b, last) if workspace is None else 0, dev, own)
+    _call("attn_prompt_weights", dev, stream, own, b, hq_, hk, pl, last, int(bool(accumulate)), po, pw, wb)
     return out
 
 

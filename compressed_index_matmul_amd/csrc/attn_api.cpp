@@ -30,7 +30,7 @@ int check_heads(const attn_heads *h, int64_t rows) {
   return VQ_OK;
 }
 
-int check_batch(const attn_batch *b, AttnView *a) {
+int check_batch(const attn_batch *b, AttnView *a, bool pointers = true) {
   if (!b) return VQ_ERR_NULL;
   if (b->dtype != VQ_BF16 && b->dtype != VQ_F16) return VQ_ERR_DTYPE;
   if (b->n_q_heads < 1 || b->n_kv_heads < 1 || b->n_q_heads % b->n_kv_heads != 0) return VQ_ERR_SHAPE;
@@ -39,8 +39,10 @@ int check_batch(const attn_batch *b, AttnView *a) {
   if (b->causal != 0 && b->causal != 1) return VQ_ERR_VALUE;
   if (!std::isfinite(b->scale) || b->scale <= 0.0f) return VQ_ERR_VALUE;
   if (!valid_head_dim(b->head_dim)) return VQ_ERR_UNSUPPORTED;
-  if (!b->cu_q || !b->cu_k) return VQ_ERR_NULL;
-  if (misaligned(b->cu_q, 4) || misaligned(b->cu_k, 4)) return VQ_ERR_ALIGN;
+  if (pointers) {
+    if (!b->cu_q || !b->cu_k) return VQ_ERR_NULL;
+    if (misaligned(b->cu_q, 4) || misaligned(b->cu_k, 4)) return VQ_ERR_ALIGN;
+  }
   *a = AttnView{};
   a->hq = b->n_q_heads;
   a->hkv = b->n_kv_heads;
@@ -126,15 +128,17 @@ using namespace vqmm;
 extern "C" {
 
 int attn_prompt(const attn_batch *b, const attn_heads *q, const attn_heads *k, const attn_heads *v, void *out,
-                float *lse, void *stream) {
+                float *lse, void *workspace, size_t ws_bytes, void *stream) {
   AttnView a;
   int st = check_batch(b, &a);
   if (st != VQ_OK) return st;
   if ((st = check_heads(q, a.tq)) != VQ_OK || (st = check_heads(k, a.tk)) != VQ_OK || (st = check_heads(v, a.tk)) != VQ_OK)
     return st;
-  if (a.tq > 0 && !out) return VQ_ERR_NULL;
-  if (misaligned(out, 16) || misaligned(lse, 4)) return VQ_ERR_ALIGN;
+  if ((a.tq > 0 && !out) || (ws_bytes > 0 && !workspace)) return VQ_ERR_NULL;
+  if (misaligned(out, 16) || misaligned(lse, 4) || misaligned(workspace, 16)) return VQ_ERR_ALIGN;
   if (!grid_fits(a.tq, a.nseq, 64, a.hq)) return VQ_ERR_SHAPE;
+  const PromptPlan p = attn_prompt_plan(a);
+  if (ws_bytes < p.bytes) return VQ_ERR_WORKSPACE;
   a.q = static_cast<const uint16_t *>(q->data);
   a.k = static_cast<const uint16_t *>(k->data);
   a.v = static_cast<const uint16_t *>(v->data);
@@ -142,26 +146,40 @@ int attn_prompt(const attn_batch *b, const attn_heads *q, const attn_heads *k, c
   a.k_ts = k->token_stride, a.k_hs = k->head_stride;
   a.v_ts = v->token_stride, a.v_hs = v->head_stride;
   if (a.tq == 0 || a.nseq == 0) return VQ_OK;
-  return map_hip(launch_attn_prompt(a, static_cast<uint16_t *>(out), lse, reinterpret_cast<hipStream_t>(stream)));
+  return map_hip(launch_attn_prompt(a, p, static_cast<uint16_t *>(out), lse, workspace, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t attn_prompt_workspace_size(const attn_batch *b) {
+  AttnView a;
+  if (check_batch(b, &a, false) != VQ_OK || !grid_fits(a.tq, a.nseq, 64, a.hq)) return 0;
+  return attn_prompt_plan(a).bytes;
 }
 
 int attn_prompt_weights(const attn_batch *b, const attn_heads *q, const attn_heads *k, const float *lse, int32_t last,
-                        int32_t accumulate, float *weights, void *stream) {
+                        int32_t accumulate, float *weights, void *workspace, size_t ws_bytes, void *stream) {
   AttnView a;
   int st = check_batch(b, &a);
   if (st != VQ_OK) return st;
   if ((st = check_heads(q, a.tq)) != VQ_OK || (st = check_heads(k, a.tk)) != VQ_OK) return st;
-  if ((a.tq > 0 && !lse) || (a.tk > 0 && !weights)) return VQ_ERR_NULL;
-  if (misaligned(lse, 4) || misaligned(weights, 4)) return VQ_ERR_ALIGN;
+  if ((a.tq > 0 && !lse) || (a.tk > 0 && !weights) || (ws_bytes > 0 && !workspace)) return VQ_ERR_NULL;
+  if (misaligned(lse, 4) || misaligned(weights, 4) || misaligned(workspace, 16)) return VQ_ERR_ALIGN;
   if (last < 0) return VQ_ERR_SHAPE;
   if (accumulate != 0 && accumulate != 1) return VQ_ERR_VALUE;
   if (!grid_fits(a.tk, a.nseq, 64, a.hkv)) return VQ_ERR_SHAPE;
+  const PromptPlan p = attn_weights_plan(a, last);
+  if (ws_bytes < p.bytes) return VQ_ERR_WORKSPACE;
   a.q = static_cast<const uint16_t *>(q->data);
   a.k = static_cast<const uint16_t *>(k->data);
   a.q_ts = q->token_stride, a.q_hs = q->head_stride;
   a.k_ts = k->token_stride, a.k_hs = k->head_stride;
   if (a.tk == 0 || a.nseq == 0) return VQ_OK;
-  return map_hip(launch_attn_weights(a, lse, last, accumulate == 1, weights, reinterpret_cast<hipStream_t>(stream)));
+  return map_hip(launch_attn_weights(a, p, lse, last, accumulate == 1, weights, workspace, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t attn_prompt_weights_workspace_size(const attn_batch *b, int32_t last) {
+  AttnView a;
+  if (check_batch(b, &a, false) != VQ_OK || last < 0 || !grid_fits(a.tk, a.nseq, 64, a.hkv)) return 0;
+  return attn_weights_plan(a, last).bytes;
 }
 
 int kv4_append(const kv4_cache *c, const kv4_seqs *s, const attn_heads *k, const attn_heads *v, int32_t dtype,

@@ -17,6 +17,8 @@
 // different banks.
 #include "attn_device.h"
 
+#include <algorithm>
+
 namespace vqmm {
 
 namespace {
@@ -62,9 +64,27 @@ struct Stage {
   }
 };
 
-template <int D, int BN, bool F16, bool CAUSAL>
-__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(AttnView a, uint16_t *__restrict__ out,
-                                                                            float *__restrict__ lse, int tiles) {
+// The pieces of a row block's keys: `piece` of them takes tiles from *lo to
+// *hi of nt, none shorter than kMinTiles but the last.
+constexpr int kMinKeys = 256;
+__device__ __forceinline__ void piece_tiles(int nt, int pieces, int piece, int bn, int *lo, int *hi) {
+  const int per = max((nt + pieces - 1) / pieces, kMinKeys / bn);
+  *lo = min(piece * per, nt);
+  *hi = min(*lo + per, nt);
+}
+
+struct PromptOut {
+  uint16_t *out;
+  float *lse;
+  float *part;  // [piece][row][head][D], sums of p v
+  float *stat;  // [piece][row][head][2]: reference maximum (log2 domain), sum of p
+};
+
+// SPLIT: the workgroup takes one piece of its keys and leaves its sums in the
+// workspace for k_attn_join.
+template <int D, int BN, bool F16, bool CAUSAL, bool SPLIT>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(AttnView a, PromptOut o, int tiles,
+                                                                            int pieces) {
   constexpr int KP = 8, VP = 32;  // padding of an LDS row, in elements
   constexpr int NS = BN / 32, ND = D / 32, NK = D / 16;
   __shared__ __attribute__((aligned(16))) uint16_t s_k[2][BN * (D + KP)];
@@ -76,6 +96,11 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(Attn
   int id = blockIdx.x;
   const int kvh = id % a.hkv;
   id /= a.hkv;
+  int piece = 0;
+  if (SPLIT) {
+    piece = id % pieces;
+    id /= pieces;
+  }
   const int group = a.hq / a.hkv;
   const int head = kvh * group + id % group;
   const int vt = tiles - 1 - id / group;
@@ -94,7 +119,11 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(Attn
   const int lim = CAUSAL ? min(qi + off, rk.n - 1) : rk.n - 1;  // last key this lane's query sees
   const int lim_first = CAUSAL ? min(qw + off, rk.n - 1) : rk.n - 1, lim_last = CAUSAL ? min(qw + 31 + off, rk.n - 1) : rk.n - 1;
   const int seen = CAUSAL ? min(q0 + kRows + off, rk.n) : rk.n;  // keys the workgroup needs
-  const int nt = seen > 0 ? (seen + BN - 1) / BN : 0;
+  int t_lo = 0, nt = seen > 0 ? (seen + BN - 1) / BN : 0;
+  if (SPLIT) {
+    piece_tiles(nt, pieces, piece, BN, &t_lo, &nt);
+    if (t_lo >= nt) return;  // an empty piece: k_attn_join knows
+  }
 
   const uint16_t *kb = a.k + rk.begin * a.k_ts + kvh * a.k_hs;
   const uint16_t *vb = a.v + rk.begin * a.v_ts + kvh * a.v_hs;
@@ -116,14 +145,14 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(Attn
 
   Stage<D, BN, KP> sk;
   Stage<D, BN, VP> sv;
-  if (nt > 0) {
-    sk.load(kb, a.k_ts, 0, seen);
-    sv.load(vb, a.v_ts, 0, seen);
-    sk.store(s_k[0]);
-    sv.store(s_v[0]);
+  if (t_lo < nt) {
+    sk.load(kb, a.k_ts, t_lo * BN, seen);
+    sv.load(vb, a.v_ts, t_lo * BN, seen);
+    sk.store(s_k[t_lo & 1]);
+    sv.store(s_v[t_lo & 1]);
   }
   __syncthreads();
-  for (int t = 0; t < nt; ++t) {
+  for (int t = t_lo; t < nt; ++t) {
     const int k0 = t * BN;
     if (t + 1 < nt) {
       sk.load(kb, a.k_ts, k0 + BN, seen);
@@ -199,9 +228,21 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(Attn
 
   lsum = sum_xor32(lsum);
   if (qi >= rq.n) return;
-  const float r = lsum == 0.0f ? 0.0f : 1.0f / lsum;
   const int64_t row = rq.begin + (int64_t)qi;
-  uint16_t *op = out + (row * a.hq + head) * D + 4 * h;
+  if (SPLIT) {
+    const int64_t at = ((int64_t)piece * a.tq + row) * a.hq + head;
+    float *pp = o.part + at * D + 4 * h;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        *reinterpret_cast<float4_t *>(pp + 32 * d + 8 * x) =
+            float4_t{acc[d][4 * x], acc[d][4 * x + 1], acc[d][4 * x + 2], acc[d][4 * x + 3]};
+    if (h == 0) *reinterpret_cast<float2_t *>(o.stat + at * 2) = float2_t{mref * cs, lsum};
+    return;
+  }
+  const float r = lsum == 0.0f ? 0.0f : 1.0f / lsum;
+  uint16_t *op = o.out + (row * a.hq + head) * D + 4 * h;
 #pragma unroll
   for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -210,25 +251,101 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(Attn
                          pack16<F16>(acc[d][4 * x + 2] * r, acc[d][4 * x + 3] * r)};
       *reinterpret_cast<uint2_t *>(op + 32 * d + 8 * x) = w;
     }
-  if (lse && h == 0)
-    lse[(int64_t)head * a.tq + row] = (mref == -INFINITY ? 0.0f : mref * a.scale) + __builtin_amdgcn_logf(lsum) * kLn2;
+  if (o.lse && h == 0)
+    o.lse[(int64_t)head * a.tq + row] = (mref == -INFINITY ? 0.0f : mref * a.scale) + __builtin_amdgcn_logf(lsum) * kLn2;
+}
+
+// The pieces meet: D / 4 lanes take one row of one head, in piece order.
+template <int D, int BN, bool F16>
+__global__ __launch_bounds__(kThreads) void k_attn_join(AttnView a, PromptOut o, int pieces) {
+  constexpr int kLanes = D / 4;
+  const int64_t at = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+  const int d = threadIdx.x % kLanes * 4;
+  if (at >= (int64_t)a.tq * a.hq) return;
+  const int row = (int)(at / a.hq), head = (int)(at % a.hq);
+  // the row's sequence: the last whose rows begin at or before it
+  int lo = 0, hi = a.nseq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (seq_rows(a.cu_q, mid, a.tq).begin <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  const Rows rq = seq_rows(a.cu_q, lo, a.tq), rk = seq_rows(a.cu_k, lo, a.tk);
+  if (row < rq.begin || row >= rq.begin + rq.n) return;
+  const int q0 = (row - rq.begin) / kRows * kRows;
+  const int seen = a.causal ? min(q0 + kRows + rk.n - rq.n, rk.n) : rk.n;
+  const int nt = seen > 0 ? (seen + BN - 1) / BN : 0;
+  const int64_t step = (int64_t)a.tq * a.hq;
+  float top = -INFINITY;
+  int np = 0;
+  for (; np < pieces; ++np) {
+    int t0, t1;
+    piece_tiles(nt, pieces, np, BN, &t0, &t1);
+    if (t0 >= t1) break;
+    top = fmaxf(top, o.stat[(np * step + at) * 2]);
+  }
+  const float m0 = top == -INFINITY ? 0.0f : top;
+  float4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  float l = 0.0f;
+  for (int p = 0; p < np; ++p) {
+    const float2_t st = *reinterpret_cast<const float2_t *>(o.stat + (p * step + at) * 2);
+    const float4_t v = *reinterpret_cast<const float4_t *>(o.part + (p * step + at) * D + d);
+    const float f = __builtin_amdgcn_exp2f(st[0] - m0);
+    l = __builtin_fmaf(st[1], f, l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] = __builtin_fmaf(v[i], f, sum[i]);
+  }
+  const float r = l == 0.0f ? 0.0f : 1.0f / l;
+  *reinterpret_cast<uint2_t *>(o.out + at * D + d) =
+      uint2_t{pack16<F16>(sum[0] * r, sum[1] * r), pack16<F16>(sum[2] * r, sum[3] * r)};
+  if (o.lse && d == 0) o.lse[(int64_t)head * a.tq + row] = (m0 + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <int D, int BN, bool F16>
-hipError_t prompt_d(const AttnView &a, uint16_t *out, float *lse, hipStream_t s) {
+hipError_t prompt_d(const AttnView &a, const PromptPlan &p, const PromptOut &o, hipStream_t s) {
   const int tiles = a.tq / kRows + a.nseq;
-  const unsigned grid = (unsigned)((int64_t)tiles * a.hq);
-  if (a.causal) k_attn_prompt<D, BN, F16, true><<<grid, kThreads, 0, s>>>(a, out, lse, tiles);
-  else k_attn_prompt<D, BN, F16, false><<<grid, kThreads, 0, s>>>(a, out, lse, tiles);
+  const int64_t blocks = (int64_t)tiles * a.hq * p.pieces;
+  if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)blocks;
+  if (p.pieces == 1) {
+    if (a.causal) k_attn_prompt<D, BN, F16, true, false><<<grid, kThreads, 0, s>>>(a, o, tiles, 1);
+    else k_attn_prompt<D, BN, F16, false, false><<<grid, kThreads, 0, s>>>(a, o, tiles, 1);
+    return hipGetLastError();
+  }
+  if (a.causal) k_attn_prompt<D, BN, F16, true, true><<<grid, kThreads, 0, s>>>(a, o, tiles, p.pieces);
+  else k_attn_prompt<D, BN, F16, false, true><<<grid, kThreads, 0, s>>>(a, o, tiles, p.pieces);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  constexpr int kRowsPerBlock = kThreads / (D / 4);
+  const int64_t rows = (int64_t)a.tq * a.hq;
+  k_attn_join<D, BN, F16><<<(unsigned)((rows + kRowsPerBlock - 1) / kRowsPerBlock), kThreads, 0, s>>>(a, o, p.pieces);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_attn_prompt(const AttnView &a, uint16_t *out, float *lse, hipStream_t s) {
-  if (a.d == 64) return a.f16 ? prompt_d<64, 64, true>(a, out, lse, s) : prompt_d<64, 64, false>(a, out, lse, s);
-  if (a.d == 128) return a.f16 ? prompt_d<128, 64, true>(a, out, lse, s) : prompt_d<128, 64, false>(a, out, lse, s);
-  return a.f16 ? prompt_d<256, 32, true>(a, out, lse, s) : prompt_d<256, 32, false>(a, out, lse, s);
+// Few row blocks (less than two a CU) are cut along the keys, into at most 8
+// pieces, where there are keys enough (1024 a piece) to pay for the second
+// launch; a short row block of such a call still keeps to pieces of 256.
+PromptPlan attn_prompt_plan(const AttnView &a) {
+  PromptPlan p{1, 0, 0};
+  const int64_t blocks = ((int64_t)a.tq / kRows + a.nseq) * a.hq;
+  const int64_t most = a.tk / 1024;
+  if (blocks > 0 && blocks < 512) p.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({768 / blocks, most, 8}));
+  if (p.pieces > 1) {
+    const size_t rows = (size_t)p.pieces * a.tq * a.hq;
+    p.stat_off = rows * a.d * 4;
+    p.bytes = p.stat_off + rows * 8;
+  }
+  return p;
+}
+
+hipError_t launch_attn_prompt(const AttnView &a, const PromptPlan &p, uint16_t *out, float *lse, void *ws, hipStream_t s) {
+  char *w = static_cast<char *>(ws);
+  const PromptOut o{out, lse, reinterpret_cast<float *>(w), reinterpret_cast<float *>(w + p.stat_off)};
+  if (a.d == 64) return a.f16 ? prompt_d<64, 64, true>(a, p, o, s) : prompt_d<64, 64, false>(a, p, o, s);
+  if (a.d == 128) return a.f16 ? prompt_d<128, 64, true>(a, p, o, s) : prompt_d<128, 64, false>(a, p, o, s);
+  return a.f16 ? prompt_d<256, 32, true>(a, p, o, s) : prompt_d<256, 32, false>(a, p, o, s);
 }
 
 }  // namespace vqmm

@@ -8,6 +8,8 @@
 // one workgroup sees all the queries of its keys: no atomics, a fixed order.
 #include "attn_device.h"
 
+#include <algorithm>
+
 namespace vqmm {
 
 namespace {
@@ -24,13 +26,14 @@ __device__ __forceinline__ float16_t mfma32(uint4_t a, uint4_t b, float16_t c) {
 
 template <int D, int BQ, bool F16, bool CAUSAL>
 __global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const float *__restrict__ lse, int last,
-                                                           int accumulate, float *__restrict__ weights) {
+                                                           int accumulate, float *__restrict__ weights, int pieces) {
   constexpr int QP = 8, NK = D / 16, NQ = BQ / 32;
   constexpr int kPieces = BQ * (D / 8) / kThreads;
   __shared__ __attribute__((aligned(16))) uint16_t s_q[2][BQ * (D + QP)];
   __shared__ __attribute__((aligned(16))) float s_lse[2][BQ];
 
-  const int kvh = blockIdx.x % a.hkv, vt = blockIdx.x / a.hkv;
+  const int kvh = blockIdx.x % a.hkv;
+  const int piece = blockIdx.x / a.hkv % pieces, vt = blockIdx.x / a.hkv / pieces;
   int first;
   const int b = find_tile(a.cu_k, a.nseq, a.tk, kKeys, 1, vt, &first);
   if (b < 0) return;
@@ -54,104 +57,138 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const flo
   int low = last > 0 ? max(0, rq.n - last) : 0;
   if (CAUSAL) low = max(low, k0 - off);
   const int ni = low < rq.n ? (rq.n - low + BQ - 1) / BQ : 0;
-  const int total = ni * group;
+  const int items = ni * group;
+  const int it0 = (int)((int64_t)items * piece / pieces), it1 = (int)((int64_t)items * (piece + 1) / pieces);
   const float cs = a.scale * kLog2e;
 
-  uint4_t stage[kPieces];
-  float stage_lse = 0.0f;
-  auto fetch = [&](int it) {
+  // Two query tiles in flight: a tile's loads go out two rounds before it is
+  // wanted, into one of two register sets, and into LDS one barrier before.
+  struct Stage {
+    uint4_t r[kPieces];
+    float lse;
+  };
+  auto fetch = [&](Stage &st, int it) {
     const int head = kvh * group + it / ni, r0 = low + it % ni * BQ;
     const uint16_t *qp = a.q + rq.begin * a.q_ts + head * a.q_hs;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int id = threadIdx.x + i * kThreads, row = r0 + id / (D / 8);
-      stage[i] = uint4_t{0, 0, 0, 0};
-      if (row < rq.n) stage[i] = *reinterpret_cast<const uint4_t *>(qp + row * a.q_ts + id % (D / 8) * 8);
+      st.r[i] = uint4_t{0, 0, 0, 0};
+      if (row < rq.n) st.r[i] = *reinterpret_cast<const uint4_t *>(qp + row * a.q_ts + id % (D / 8) * 8);
     }
     if (threadIdx.x < BQ) {
       // rows past the end, and rows without keys, give exp2(-inf) = 0
       const int row = r0 + threadIdx.x;
       const float v = row < rq.n ? lse[(int64_t)head * a.tq + rq.begin + row] : -INFINITY;
-      stage_lse = v == -INFINITY ? INFINITY : v * kLog2e;
+      st.lse = v == -INFINITY ? INFINITY : v * kLog2e;
     }
   };
-  auto put = [&](int buf) {
+  float sum = 0.0f;
+  auto step = [&](Stage &st, int it) {
+    const int buf = it & 1;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int id = threadIdx.x + i * kThreads;
-      *reinterpret_cast<uint4_t *>(&s_q[buf][(id / (D / 8)) * (D + QP) + id % (D / 8) * 8]) = stage[i];
+      *reinterpret_cast<uint4_t *>(&s_q[buf][(id / (D / 8)) * (D + QP) + id % (D / 8) * 8]) = st.r[i];
     }
-    if (threadIdx.x < BQ) s_lse[buf][threadIdx.x] = stage_lse;
-  };
-
-  float sum = 0.0f;
-  if (total > 0) {
-    fetch(0);
-    put(0);
-  }
-  __syncthreads();
-  for (int it = 0; it < total; ++it) {
-    if (it + 1 < total) fetch(it + 1);
+    if (threadIdx.x < BQ) s_lse[buf][threadIdx.x] = st.lse;
+    __syncthreads();
+    if (it + 2 < it1) fetch(st, it + 2);
     const int r0 = low + it % ni * BQ;
-    const bool some = !CAUSAL || r0 + BQ - 1 + off >= kw;  // some query of the tile sees some key of the wave
-    if (some) {
-      const bool mask = r0 + BQ > rq.n || (CAUSAL && r0 + off < kw + 31);
-      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (CAUSAL && r0 + BQ - 1 + off < kw) return;  // no query of the tile sees a key of the wave
+    const bool mask = r0 + BQ > rq.n || (CAUSAL && r0 + off < kw + 31);
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        float16_t S;
+    for (int n = 0; n < NQ; ++n) {
+      float16_t S;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) S[r] = 0.0f;
-        const uint16_t *qs = &s_q[it & 1][(32 * n + col) * (D + QP) + 8 * h];
+      for (int r = 0; r < 16; ++r) S[r] = 0.0f;
+      const uint16_t *qs = &s_q[buf][(32 * n + col) * (D + QP) + 8 * h];
 #pragma unroll
-        for (int i = 0; i < NK; ++i) S = mfma32<F16>(*reinterpret_cast<const uint4_t *>(qs + 16 * i), kf[i], S);
+      for (int i = 0; i < NK; ++i) S = mfma32<F16>(*reinterpret_cast<const uint4_t *>(qs + 16 * i), kf[i], S);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int q8 = 32 * n + 8 * x + 4 * h;
-          const float4_t l4 = *reinterpret_cast<const float4_t *>(&s_lse[it & 1][q8]);
+      for (int x = 0; x < 4; ++x) {
+        const int q8 = 32 * n + 8 * x + 4 * h;
+        const float4_t l4 = *reinterpret_cast<const float4_t *>(&s_lse[buf][q8]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float p = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * x + i], cs, -l4[i]));
-            if (mask) {
-              const int row = r0 + q8 + i;
-              p = row < rq.n && (!CAUSAL || ki <= row + off) ? p : 0.0f;
-            }
-            part[i] += p;
+        for (int i = 0; i < 4; ++i) {
+          float p = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * x + i], cs, -l4[i]));
+          if (mask) {
+            const int row = r0 + q8 + i;
+            p = row < rq.n && (!CAUSAL || ki <= row + off) ? p : 0.0f;
           }
+          part[i] += p;
         }
       }
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
     }
-    if (it + 1 < total) put((it + 1) & 1);
-    __syncthreads();
+    sum += (part[0] + part[1]) + (part[2] + part[3]);
+  };
+  Stage st0, st1;
+  if (it0 < it1) fetch(st0, it0);
+  if (it0 + 1 < it1) fetch(st1, it0 + 1);
+  for (int it = it0; it < it1; it += 2) {
+    step(st0, it);
+    if (it + 1 < it1) step(st1, it + 1);
   }
   sum = sum_xor32(sum);
   if (h == 0 && ki < rk.n) {
-    float *w = weights + (int64_t)kvh * a.tk + rk.begin + ki;
+    float *w = weights + ((int64_t)piece * a.hkv + kvh) * a.tk + rk.begin + ki;
     *w = accumulate ? *w + sum : sum;
   }
 }
 
+// Pieces of the queries meet, in order.
+__global__ __launch_bounds__(kThreads) void k_attn_weights_join(const float *__restrict__ part, int64_t n, int pieces,
+                                                                int accumulate, float *__restrict__ weights) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;
+  float sum = 0.0f;
+  for (int p = 0; p < pieces; ++p) sum += part[p * n + i];
+  weights[i] = accumulate ? weights[i] + sum : sum;
+}
+
 template <int D, int BQ, bool F16>
-hipError_t weights_d(const AttnView &a, const float *lse, int last, bool accumulate, float *weights, hipStream_t s) {
-  const unsigned grid = (unsigned)((int64_t)(a.tk / kKeys + a.nseq) * a.hkv);
-  if (a.causal) k_attn_weights<D, BQ, F16, true><<<grid, kThreads, 0, s>>>(a, lse, last, accumulate, weights);
-  else k_attn_weights<D, BQ, F16, false><<<grid, kThreads, 0, s>>>(a, lse, last, accumulate, weights);
+hipError_t weights_d(const AttnView &a, const PromptPlan &p, const float *lse, int last, bool accumulate, float *weights,
+                     float *ws, hipStream_t s) {
+  const int64_t blocks = (int64_t)(a.tk / kKeys + a.nseq) * a.hkv * p.pieces;
+  if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)blocks;
+  const int64_t n = (int64_t)a.hkv * a.tk;
+  float *to = p.pieces > 1 ? ws : weights;
+  const int add = p.pieces == 1 && accumulate;
+  if (a.causal) k_attn_weights<D, BQ, F16, true><<<grid, kThreads, 0, s>>>(a, lse, last, add, to, p.pieces);
+  else k_attn_weights<D, BQ, F16, false><<<grid, kThreads, 0, s>>>(a, lse, last, add, to, p.pieces);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.pieces == 1) return e;
+  k_attn_weights_join<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(ws, n, p.pieces, accumulate, weights);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_attn_weights(const AttnView &a, const float *lse, int last, bool accumulate, float *weights,
-                               hipStream_t s) {
+// Few key blocks (less than two a CU) are cut along the queries, into at
+// most 16 pieces of at least one tile.
+PromptPlan attn_weights_plan(const AttnView &a, int last) {
+  PromptPlan p{1, 0, 0};
+  const int64_t blocks = ((int64_t)a.tk / kKeys + a.nseq) * a.hkv;
+  const int64_t queries = last > 0 ? std::min(last, a.tq) : a.tq;
+  const int64_t most = (queries + 63) / 64 * (a.hq / a.hkv);
+  if (blocks > 0 && blocks < 512 && most > 1) p.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({512 / blocks, most, 16}));
+  if (p.pieces > 1) p.bytes = (size_t)p.pieces * a.hkv * a.tk * 4;
+  return p;
+}
+
+hipError_t launch_attn_weights(const AttnView &a, const PromptPlan &p, const float *lse, int last, bool accumulate,
+                               float *weights, void *ws, hipStream_t s) {
+  float *w = static_cast<float *>(ws);
   if (a.d == 64)
-    return a.f16 ? weights_d<64, 64, true>(a, lse, last, accumulate, weights, s)
-                 : weights_d<64, 64, false>(a, lse, last, accumulate, weights, s);
+    return a.f16 ? weights_d<64, 64, true>(a, p, lse, last, accumulate, weights, w, s)
+                 : weights_d<64, 64, false>(a, p, lse, last, accumulate, weights, w, s);
   if (a.d == 128)
-    return a.f16 ? weights_d<128, 64, true>(a, lse, last, accumulate, weights, s)
-                 : weights_d<128, 64, false>(a, lse, last, accumulate, weights, s);
-  return a.f16 ? weights_d<256, 32, true>(a, lse, last, accumulate, weights, s)
-               : weights_d<256, 32, false>(a, lse, last, accumulate, weights, s);
+    return a.f16 ? weights_d<128, 64, true>(a, p, lse, last, accumulate, weights, w, s)
+                 : weights_d<128, 64, false>(a, p, lse, last, accumulate, weights, w, s);
+  return a.f16 ? weights_d<256, 32, true>(a, p, lse, last, accumulate, weights, w, s)
+               : weights_d<256, 32, false>(a, p, lse, last, accumulate, weights, w, s);
 }
 
 }  // namespace vqmm

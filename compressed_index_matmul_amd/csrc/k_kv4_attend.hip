@@ -29,6 +29,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kTile = 32;  // slots a wave takes at a time
+constexpr int kPieces = 3072;
 constexpr float kSlack = 8.0f;  // the reference maximum lags by up to 2^8: p <= 256 is in fp16's range
 
 // dword N of the 16 lanes of a row, in all of them.
@@ -141,7 +142,7 @@ struct AttendArgs {
 };
 
 template <int D, bool F16, bool WEIGH>
-__global__ __launch_bounds__(kThreads) void k_kv4_attend(KvView c, AttendPlan p, AttendArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void k_kv4_attend(KvView c, AttendPlan p, AttendArgs a) {
   constexpr int DG = D / 32, CH = D / 16;
   constexpr int kPitch = D + 4;  // floats of a head's row in LDS: 16-byte pieces of 16 rows fall on different banks
   __shared__ float s_o[kWaves][16][kPitch];
@@ -159,7 +160,7 @@ __global__ __launch_bounds__(kThreads) void k_kv4_attend(KvView c, AttendPlan p,
 
   const int len = min(max(c.lens[b], 0), p.len_cap);
   const int ntiles = (len + kTile - 1) / kTile;
-  const int t_begin = (int)((int64_t)ntiles * split / p.splits), t_end = (int)((int64_t)ntiles * (split + 1) / p.splits);
+  const int t_begin = min(split * p.tiles, ntiles), t_end = min(t_begin + p.tiles, ntiles);
   const int heads = min(16, p.group - ht * 16);   // of this workgroup
   const int head0 = kvh * p.group + ht * 16;
   const int col = lane & 15, h4 = lane >> 4;
@@ -455,11 +456,14 @@ AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add
   p.group = n_q_heads / c.hkv;
   p.htiles = (p.group + 15) / 16;
   p.len_cap = (int)std::min<int64_t>(max_len, (int64_t)c.mp * c.ps);
-  // enough pieces to give every CU four workgroups, none shorter than the
-  // 128 slots that its waves take in one round
+  // Pieces of equal size, so that sequences of unequal length spread evenly: about 3072 of them (twelve
+  // workgroups a CU) if every sequence were as long as the bound, but not below the 128 slots that the waves
+  // take in one round.
   const int64_t work = (int64_t)c.nseq * c.hkv * p.htiles;
-  const int64_t want = (4 * 256 + work - 1) / work, most = ((int64_t)p.len_cap + kWaves * kTile - 1) / (kWaves * kTile);
-  p.splits = (int)std::max<int64_t>(1, std::min(want, most));
+  const int64_t round_slots = kWaves * kTile;
+  const int64_t rounds = std::max<int64_t>(1, ((int64_t)p.len_cap * work + kPieces * round_slots - 1) / (kPieces * round_slots));
+  p.tiles = (int)std::min<int64_t>(rounds * kWaves, ((int64_t)1 << 26));
+  p.splits = (int)std::max<int64_t>(1, ((int64_t)p.len_cap + p.tiles * kTile - 1) / ((int64_t)p.tiles * kTile));
   p.score_pitch = (p.len_cap + kTile - 1) / kTile * kTile;
   const size_t rows = (size_t)c.nseq * n_q_heads;
   auto round = [](size_t x) { return (x + 255) & ~(size_t)255; };

@@ -21,7 +21,8 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / kWave;
 constexpr int kMoveThreads = 256;
-constexpr int kMovesPerBlock = 16;
+constexpr int kMovesPerBlock = kMoveThreads / kWave;
+constexpr int kFuseMoves = 16;  // at most one a wave of the selecting workgroup
 
 // Keys in the order of the weights: NaN lowest, the protected slots on top.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -40,48 +41,132 @@ __device__ __forceinline__ int wave_prefix(int *s, int wave, int count) {
   return before;
 }
 
+// Copies slot src to slot dst, by one wave: keys and steps of both kinds,
+// weight and position.
+template <int D>
+__device__ __forceinline__ void move_slot(const KvView &c, int b, int kvh, int src, int dst, int lane) {
+  constexpr int DG = D / 32;
+  const int64_t code_head = (int64_t)c.ps * (D / 2), scale_head = (int64_t)c.ps * (DG * 2);
+  const int sp = src / c.ps, dp = dst / c.ps;
+  const int so = src - sp * c.ps, d_o = dst - dp * c.ps;
+  const int64_t spage = page_of(c, b, sp), dpage = page_of(c, b, dp);
+  const uint8_t *sc = c.codes + (spage * 2 * c.hkv + kvh) * code_head;
+  uint8_t *dc = c.codes + (dpage * 2 * c.hkv + kvh) * code_head;
+  const uint16_t *ss = c.scales + (spage * 2 * c.hkv + kvh) * scale_head;
+  uint16_t *ds = c.scales + (dpage * 2 * c.hkv + kvh) * scale_head;
+  const int64_t sa = (spage * c.hkv + kvh) * c.ps + so, da = (dpage * c.hkv + kvh) * c.ps + d_o;
+  const int sb = (so & 3) == 1 ? 2 : (so & 3) == 2 ? 1 : so & 3, db = (d_o & 3) == 1 ? 2 : (d_o & 3) == 2 ? 1 : d_o & 3;
+  const uint8_t *sv = sc + c.hkv * code_head + (so >> 2) * (2 * D) + sb;
+  uint8_t *dv = dc + c.hkv * code_head + (d_o >> 2) * (2 * D) + db;
+  constexpr int NV = (D / 2 + kWave - 1) / kWave;
+  // every load first: their latencies overlap
+  uint32_t key = 0;
+  uint16_t sm = 0;
+  uint8_t val[NV] = {};
+  float w = 0.0f;
+  int32_t at = 0;
+  const int kind = lane / (2 * DG), gs = lane % (2 * DG);  // (kind, group, step or minimum)
+  const int64_t k0 = kind * c.hkv * scale_head + gs * 4;
+  if (lane < D / 8) key = reinterpret_cast<const uint32_t *>(sc + so * (D / 2))[lane];
+#pragma unroll
+  for (int x = 0; x < NV; ++x)
+    if (x * kWave + lane < D / 2) val[x] = sv[(x * kWave + lane) * 4];
+  if (lane < 4 * DG) sm = ss[k0 + (so >> 2) * (DG * 8) + (so & 3)];
+  if (lane == 62) w = c.weights[sa];
+  if (lane == 63) at = c.pos[sa];
+  if (lane < D / 8) reinterpret_cast<uint32_t *>(dc + d_o * (D / 2))[lane] = key;
+#pragma unroll
+  for (int x = 0; x < NV; ++x)
+    if (x * kWave + lane < D / 2) dv[(x * kWave + lane) * 4] = val[x];
+  if (lane < 4 * DG) ds[k0 + (d_o >> 2) * (DG * 8) + (d_o & 3)] = sm;
+  if (lane == 62) c.weights[da] = w;
+  if (lane == 63) c.pos[da] = at;
+}
+
+// A wave's run of slots, 64 at a time, and where their keys are kept: in
+// registers (R > 0: up to 1024 R slots) or in the workspace (R = 0).
+template <int R>
+struct Keys {
+  uint32_t r[R];
+  __device__ __forceinline__ uint32_t get(int i, const uint32_t *, int) const { return r[i]; }
+  __device__ __forceinline__ void set(int i, uint32_t *, int, uint32_t k) { r[i] = k; }
+};
+template <>
+struct Keys<0> {
+  __device__ __forceinline__ uint32_t get(int, const uint32_t *ws, int slot) const { return ws[slot]; }
+  __device__ __forceinline__ void set(int, uint32_t *ws, int slot, uint32_t k) { ws[slot] = k; }
+};
+
+// f(i, slot) for the steps i of the wave's run; unrolled where the keys are registers.
+template <int R, typename F>
+__device__ __forceinline__ void each_step(int steps, int first, F f) {
+  if (R > 0) {
+#pragma unroll
+    for (int i = 0; i < (R > 0 ? R : 1); ++i)
+      if (i < steps) f(i, first + i * kWave);
+  } else {
+    for (int i = 0; i < steps; ++i) f(i, first + i * kWave);
+  }
+}
+
+constexpr int kCopies = 4;  // histograms of a wave: equal digits of neighbouring lanes fall on different counters
+
+// FUSE > 0: the workgroup moves its few slots itself, head_dim FUSE.
+template <int R, int FUSE>
 __global__ __launch_bounds__(kSelThreads) void k_kv4_select(KvView c, EvictPlan p, const int32_t *__restrict__ next_pos,
                                                             int keep, int recent, uint32_t *__restrict__ keys_all,
                                                             int32_t *__restrict__ moves, int32_t *__restrict__ counts) {
-  __shared__ int s_hist[kSelWaves][256];
+  __shared__ int s_hist[kSelWaves / 4][kCopies][256];
   __shared__ int s_sum[256];
   __shared__ int s_wave[kSelWaves];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
+  __shared__ int s_to[FUSE ? kFuseMoves : 1], s_from[FUSE ? kFuseMoves : 1];
 
   const int row = blockIdx.x;
   const int b = row / c.hkv, kvh = row - b * c.hkv;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int len = min(max(c.lens[b], 0), p.len_cap);
   if (len <= keep) {
-    if (tid == 0) counts[row] = 0;
+    if (!FUSE && tid == 0) counts[row] = 0;
     return;
   }
-  uint32_t *keys = keys_all + (int64_t)row * p.len_cap;
+  uint32_t *ws = keys_all + (int64_t)row * p.len_cap;
   const int64_t oldest = (int64_t)next_pos[b] - recent;  // positions from here on are kept
+  const int steps = (len + kSelThreads - 1) / kSelThreads;
+  const int first = wave * steps * kWave + lane;
+
+  // Keys in the order of the weights, protected slots on top; lanes past the
+  // end hold 0 and count nowhere (a NaN's 0 does count: `slot < len` is asked).
+  Keys<R> keys;
+  const int tiles = c.ps / 32;
+  each_step<R>(steps, first, [&](int i, int slot) {
+    uint32_t key = 0;
+    if (slot < len) {
+      const int pi = (slot >> 5) / tiles;
+      const int64_t at = (page_of(c, b, pi) * c.hkv + kvh) * c.ps + (slot - pi * c.ps);
+      key = c.pos[at] >= oldest ? 0xffffffffu : weight_key(c.weights[at]);
+    }
+    if (R > 0 || slot < len) keys.set(i, ws, slot, key);
+  });
 
   uint32_t prefix = 0;
   int need = keep;
+  int *hist = s_hist[wave / 4][lane % kCopies];
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < kSelWaves * 256; i += kSelThreads) (&s_hist[0][0])[i] = 0;
+    for (int i = tid; i < kSelWaves / 4 * kCopies * 256; i += kSelThreads) (&s_hist[0][0][0])[i] = 0;
     __syncthreads();
-    for (int slot = tid; slot < len; slot += kSelThreads) {
-      uint32_t key;
-      if (shift == 24) {
-        const int pi = slot / c.ps;
-        const int64_t at = (page_of(c, b, pi) * c.hkv + kvh) * c.ps + (slot - pi * c.ps);
-        key = c.pos[at] >= oldest ? 0xffffffffu : weight_key(c.weights[at]);
-        keys[slot] = key;
-      } else {
-        key = keys[slot];
+    each_step<R>(steps, first, [&](int i, int slot) {
+      if (slot < len) {
+        const uint32_t key = keys.get(i, ws, slot);
+        if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255u], 1);
       }
-      if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_hist[wave][(key >> shift) & 255u], 1);
-    }
+    });
     __syncthreads();
     if (tid < 256) {
       int n = 0;
 #pragma unroll
-      for (int w = 0; w < kSelWaves; ++w) n += s_hist[w][tid];
+      for (int w = 0; w < kSelWaves / 4 * kCopies; ++w) n += (&s_hist[0][0][0])[w * 256 + tid];
       s_sum[tid] = n;
     }
     __syncthreads();
@@ -108,85 +193,84 @@ __global__ __launch_bounds__(kSelThreads) void k_kv4_select(KvView c, EvictPlan 
     __syncthreads();
     prefix = s_prefix;
     need = s_need;
-    __syncthreads();
   }
 
-  // a wave's run of slots: ties first, then the lists
-  const int run = ((len + kSelWaves - 1) / kSelWaves + kWave - 1) / kWave * kWave;
-  const int lo = min(wave * run, len), hi = min(lo + run, len);
+  // ties of the keep-th key by slot, then the two lists
   const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
   int ties = 0;
-  for (int s0 = lo; s0 < hi; s0 += kWave) {
-    const int slot = s0 + lane;
-    ties += __popcll(__ballot(slot < hi && keys[slot] == prefix));
-  }
+  each_step<R>(steps, first, [&](int i, int slot) {
+    ties += __popcll(__ballot(slot < len && keys.get(i, ws, min(slot, len - 1)) == prefix));
+  });
   const int ties_before = wave_prefix(s_wave, wave, ties);
-  int holes = 0, movers = 0, holes_at = 0, movers_at = 0;
+  int holes_at = 0, movers_at = 0;
   int32_t *to = moves + (int64_t)row * 2 * p.max_moves, *from = to + p.max_moves;
+#pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
     int t = ties_before, h = holes_at, m = movers_at;
-    for (int s0 = lo; s0 < hi; s0 += kWave) {
-      const int slot = s0 + lane;
-      const bool in = slot < hi;
-      const uint32_t key = in ? keys[slot] : 0u;
+    each_step<R>(steps, first, [&](int i, int slot) {
+      const bool in = slot < len;
+      const uint32_t key = keys.get(i, ws, min(slot, len - 1));
       const uint64_t tie = __ballot(in && key == prefix);
       const bool stays = in && (key > prefix || (key == prefix && t + __popcll(tie & below) < need));
       t += __popcll(tie);
-      const uint64_t hole = __ballot(in && !stays && slot < keep), mover = __ballot(stays && slot >= keep);
+      const bool is_hole = in && !stays && slot < keep, is_mover = stays && slot >= keep;
+      const uint64_t hole = __ballot(is_hole), mover = __ballot(is_mover);
       if (pass == 1) {
-        if (in && !stays && slot < keep) to[h + __popcll(hole & below)] = slot;
-        if (stays && slot >= keep) from[m + __popcll(mover & below)] = slot;
+        const int hi = h + __popcll(hole & below), mi = m + __popcll(mover & below);
+        if (is_hole) FUSE ? s_to[hi] = slot : to[hi] = slot;
+        if (is_mover) FUSE ? s_from[mi] = slot : from[mi] = slot;
       }
       h += __popcll(hole);
       m += __popcll(mover);
-    }
+    });
     if (pass == 0) {
-      holes = h;
-      movers = m;
-      holes_at = wave_prefix(s_wave, wave, holes);
-      movers_at = wave_prefix(s_wave, wave, movers);
-      if (wave == kSelWaves - 1 && lane == 0) counts[row] = min(movers_at + movers, p.max_moves);
+      holes_at = wave_prefix(s_wave, wave, h);
+      movers_at = wave_prefix(s_wave, wave, m);
+      if (wave == kSelWaves - 1 && lane == 0) {
+        if (FUSE) s_need = movers_at + m;
+        else counts[row] = movers_at + m;
+      }
     }
+  }
+  if (FUSE) {
+    __syncthreads();
+    for (int i = wave; i < s_need; i += kSelWaves) move_slot<FUSE ? FUSE : 64>(c, b, kvh, s_from[i], s_to[i], lane);
   }
 }
 
 template <int D>
 __global__ __launch_bounds__(kMoveThreads) void k_kv4_move(KvView c, EvictPlan p, const int32_t *__restrict__ moves,
                                                            const int32_t *__restrict__ counts, int chunks) {
-  constexpr int DG = D / 32;
   const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
-  const int b = row / c.hkv, kvh = row - b * c.hkv;
-  const int n = counts[row], lane = threadIdx.x & 63;
+  const int i = chunk * kMovesPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (i >= counts[row]) return;
   const int32_t *to = moves + (int64_t)row * 2 * p.max_moves, *from = to + p.max_moves;
-  const int64_t code_head = (int64_t)c.ps * (D / 2), scale_head = (int64_t)c.ps * (DG * 2);
-  for (int w = threadIdx.x >> 6; w < kMovesPerBlock; w += kMoveThreads / kWave) {
-    const int i = chunk * kMovesPerBlock + w;
-    if (i >= n) return;
-    const int src = from[i], dst = to[i];
-    const int sp = src / c.ps, dp = dst / c.ps;
-    const int so = src - sp * c.ps, d_o = dst - dp * c.ps;
-    const int64_t spage = page_of(c, b, sp), dpage = page_of(c, b, dp);
-    uint8_t *sc = c.codes + (spage * 2 * c.hkv + kvh) * code_head, *dc = c.codes + (dpage * 2 * c.hkv + kvh) * code_head;
-    uint16_t *ss = c.scales + (spage * 2 * c.hkv + kvh) * scale_head;
-    uint16_t *ds = c.scales + (dpage * 2 * c.hkv + kvh) * scale_head;
-    if (lane < D / 8)
-      reinterpret_cast<uint32_t *>(dc + (int64_t)d_o * (D / 2))[lane] =
-          reinterpret_cast<const uint32_t *>(sc + (int64_t)so * (D / 2))[lane];
-    sc += c.hkv * code_head, dc += c.hkv * code_head;
-    const int sb = (so & 3) == 1 ? 2 : (so & 3) == 2 ? 1 : so & 3, db = (d_o & 3) == 1 ? 2 : (d_o & 3) == 2 ? 1 : d_o & 3;
-#pragma unroll
-    for (int x = 0; x < D / 2; x += kWave)
-      if (x + lane < D / 2)
-        dc[(int64_t)(d_o >> 2) * (2 * D) + (x + lane) * 4 + db] = sc[(int64_t)(so >> 2) * (2 * D) + (x + lane) * 4 + sb];
-    if (lane < 4 * DG) {  // (kind, group, step or minimum)
-      const int kind = lane / (2 * DG), gs = lane % (2 * DG);
-      const int64_t k0 = kind * c.hkv * scale_head;
-      ds[k0 + (d_o >> 2) * (DG * 8) + gs * 4 + (d_o & 3)] = ss[k0 + (so >> 2) * (DG * 8) + gs * 4 + (so & 3)];
-    }
-    const int64_t sa = (spage * c.hkv + kvh) * c.ps + so, da = (dpage * c.hkv + kvh) * c.ps + d_o;
-    if (lane == 62) c.weights[da] = c.weights[sa];
-    if (lane == 63) c.pos[da] = c.pos[sa];
+  move_slot<D>(c, row / c.hkv, row % c.hkv, from[i], to[i], threadIdx.x & 63);
+}
+
+template <int R, int FUSE>
+hipError_t select_rows(const KvView &c, const EvictPlan &p, const int32_t *next_pos, int keep, int recent, uint32_t *keys,
+                       int32_t *moves, int32_t *counts, hipStream_t s) {
+  k_kv4_select<R, FUSE><<<c.nseq * c.hkv, kSelThreads, 0, s>>>(c, p, next_pos, keep, recent, keys, moves, counts);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t evict_d(const KvView &c, const EvictPlan &p, const int32_t *next_pos, int keep, int recent, uint32_t *keys,
+                   int32_t *moves, int32_t *counts, hipStream_t s) {
+  const int rows = c.nseq * c.hkv;
+  if (p.max_moves <= kFuseMoves) {
+    if (p.len_cap <= 2 * kSelThreads) return select_rows<2, D>(c, p, next_pos, keep, recent, keys, moves, counts, s);
+    if (p.len_cap <= 16 * kSelThreads) return select_rows<16, D>(c, p, next_pos, keep, recent, keys, moves, counts, s);
   }
+  hipError_t e = p.len_cap <= 16 * kSelThreads   ? select_rows<16, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
+                 : p.len_cap <= 32 * kSelThreads ? select_rows<32, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
+                                                 : select_rows<0, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s);
+  if (e != hipSuccess) return e;
+  const int chunks = (p.max_moves + kMovesPerBlock - 1) / kMovesPerBlock;
+  if ((int64_t)rows * chunks >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+  k_kv4_move<D><<<(unsigned)(rows * chunks), kMoveThreads, 0, s>>>(c, p, moves, counts, chunks);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -209,16 +293,9 @@ hipError_t launch_kv4_evict(const KvView &c, const EvictPlan &p, const int32_t *
   char *w = static_cast<char *>(ws);
   uint32_t *keys = reinterpret_cast<uint32_t *>(w + p.key_off);
   int32_t *moves = reinterpret_cast<int32_t *>(w + p.move_off), *counts = reinterpret_cast<int32_t *>(w + p.count_off);
-  const int rows = c.nseq * c.hkv;
-  const int chunks = (p.max_moves + kMovesPerBlock - 1) / kMovesPerBlock;
-  if ((int64_t)rows * chunks >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
-  k_kv4_select<<<rows, kSelThreads, 0, s>>>(c, p, next_pos, keep, recent, keys, moves, counts);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (c.d == 64) k_kv4_move<64><<<rows * chunks, kMoveThreads, 0, s>>>(c, p, moves, counts, chunks);
-  else if (c.d == 128) k_kv4_move<128><<<rows * chunks, kMoveThreads, 0, s>>>(c, p, moves, counts, chunks);
-  else k_kv4_move<256><<<rows * chunks, kMoveThreads, 0, s>>>(c, p, moves, counts, chunks);
-  return hipGetLastError();
+  if (c.d == 64) return evict_d<64>(c, p, next_pos, keep, recent, keys, moves, counts, s);
+  if (c.d == 128) return evict_d<128>(c, p, next_pos, keep, recent, keys, moves, counts, s);
+  return evict_d<256>(c, p, next_pos, keep, recent, keys, moves, counts, s);
 }
 
 }  // namespace vqmm

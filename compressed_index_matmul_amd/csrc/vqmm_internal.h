@@ -100,9 +100,17 @@ struct AttnView {
   const uint16_t *q, *k, *v;
   int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;  // strides in elements
 };
-hipError_t launch_attn_prompt(const AttnView &a, uint16_t *out, float *lse, hipStream_t s);
-hipError_t launch_attn_weights(const AttnView &a, const float *lse, int last, bool accumulate, float *weights,
-                               hipStream_t s);
+// Pieces that the keys (attn_prompt) or the queries (attn_prompt_weights) of
+// a workgroup's rows are cut into, a function of sizes only; 1: no workspace.
+struct PromptPlan {
+  int pieces;
+  size_t stat_off, bytes;
+};
+PromptPlan attn_prompt_plan(const AttnView &a);
+PromptPlan attn_weights_plan(const AttnView &a, int last);
+hipError_t launch_attn_prompt(const AttnView &a, const PromptPlan &p, uint16_t *out, float *lse, void *ws, hipStream_t s);
+hipError_t launch_attn_weights(const AttnView &a, const PromptPlan &p, const float *lse, int last, bool accumulate,
+                               float *weights, void *ws, hipStream_t s);
 
 // A validated cache with its sequences.
 struct KvView {
@@ -125,7 +133,8 @@ hipError_t launch_kv4_read(const KvView &c, const int32_t *cu, int total, int dt
 struct AttendPlan {
   int group;        // query heads per key/value head
   int htiles;       // 16-head tiles of a group
-  int splits;       // pieces of the slots of one sequence and head
+  int tiles;        // 32-slot tiles of one piece of a sequence and head
+  int splits;       // pieces that the longest sequence may have
   int len_cap;      // lengths are clamped to this
   int score_pitch;  // floats per head of stored scores (add_weights)
   size_t part_off, stat_off, score_off, bytes;

@@ -437,9 +437,16 @@ typedef struct attn_batch {
  * maximum and sum and the output sum are fp32; the probabilities enter the
  * second product rounded to the 16-bit type of v.  Key rows outside a
  * sequence never reach its result, whatever they hold.
+ *   workspace : 16-byte aligned, at least attn_prompt_workspace_size bytes
+ *               (NULL when that is 0): where few rows meet many keys, their
+ *               keys are cut into pieces that meet in a second launch
  */
 int attn_prompt(const attn_batch *b, const attn_heads *q, const attn_heads *k, const attn_heads *v, void *out,
-                float *lse, void *stream);
+                float *lse, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace attn_prompt needs; 0 for none and for sizes it refuses
+ * (the pointers of b are not looked at).  Host only. */
+size_t attn_prompt_workspace_size(const attn_batch *b);
 
 /*
  * The attention weight each key gathers from a prompt's queries:
@@ -449,10 +456,16 @@ int attn_prompt(const attn_batch *b, const attn_heads *q, const attn_heads *k, c
  *   lse        : float [n_q_heads][total_q], as attn_prompt gives it
  *   accumulate : 0 writes weights, 1 adds to them
  *   weights    : float [n_kv_heads][total_k]
+ *   workspace  : 16-byte aligned, at least attn_prompt_weights_workspace_size
+ *                bytes (NULL when that is 0): where few keys meet many
+ *                queries, pieces of the queries meet in a second launch
  * fp32 throughout but for the 16-bit q and k.
  */
 int attn_prompt_weights(const attn_batch *b, const attn_heads *q, const attn_heads *k, const float *lse, int32_t last,
-                        int32_t accumulate, float *weights, void *stream);
+                        int32_t accumulate, float *weights, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace attn_prompt_weights needs; as above.  Host only. */
+size_t attn_prompt_weights_workspace_size(const attn_batch *b, int32_t last);
 
 /* ----------------------------------------------------------------------
  * The 4-bit cache.  A pool of pages of page_size slots; a slot holds one

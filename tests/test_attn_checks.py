@@ -46,9 +46,9 @@ ROW_ERRORS = [(dict(data=None), NULL), (dict(data=FAKE + 8), ALIGN), (dict(ts=0)
 
 @pytest.mark.parametrize("kw,want", BATCH_ERRORS)
 def test_prompt_batch(L, kw, want):
-    assert L.attn_prompt(batch(**kw), rows(), rows(), rows(), FAKE, None, None) == want
+    assert L.attn_prompt(batch(**kw), rows(), rows(), rows(), FAKE, None, FAKE, 1 << 40, None) == want
     if "total_q" not in kw or kw["total_q"] < 0:
-        assert L.attn_prompt_weights(batch(**kw), rows(), rows(), FAKE, 0, 0, FAKE, None) == want
+        assert L.attn_prompt_weights(batch(**kw), rows(), rows(), FAKE, 0, 0, FAKE, FAKE, 1 << 40, None) == want
 
 
 @pytest.mark.parametrize("kw,want", ROW_ERRORS)
@@ -56,26 +56,46 @@ def test_prompt_rows(L, kw, want):
     for i in range(3):
         h = [rows(), rows(), rows()]
         h[i] = rows(**kw)
-        assert L.attn_prompt(batch(), *h, FAKE, None, None) == want
+        assert L.attn_prompt(batch(), *h, FAKE, None, FAKE, 1 << 40, None) == want
         if i < 2:
-            assert L.attn_prompt_weights(batch(), *h[:2], FAKE, 0, 0, FAKE, None) == want
+            assert L.attn_prompt_weights(batch(), *h[:2], FAKE, 0, 0, FAKE, FAKE, 1 << 40, None) == want
+
+
+def prompt(L, b=None, q=None, out=FAKE, lse=None, ws=FAKE, n=1 << 40):
+    return L.attn_prompt(b or batch(), q or rows(), rows(), rows(), out, lse, ws, n, None)
+
+
+def gather(L, b=None, lse=FAKE, last=0, accumulate=0, out=FAKE, ws=FAKE, n=1 << 40):
+    return L.attn_prompt_weights(b or batch(), rows(), rows(), lse, last, accumulate, out, ws, n, None)
 
 
 def test_prompt_pointers(L):
-    assert L.attn_prompt(None, rows(), rows(), rows(), FAKE, None, None) == NULL
-    assert L.attn_prompt(batch(), None, rows(), rows(), FAKE, None, None) == NULL
-    assert L.attn_prompt(batch(), rows(), rows(), rows(), None, None, None) == NULL
-    assert L.attn_prompt(batch(), rows(), rows(), rows(), FAKE + 2, None, None) == ALIGN
-    assert L.attn_prompt(batch(), rows(), rows(), rows(), FAKE, FAKE + 2, None) == ALIGN
-    assert L.attn_prompt_weights(batch(), rows(), rows(), None, 0, 0, FAKE, None) == NULL
-    assert L.attn_prompt_weights(batch(), rows(), rows(), FAKE, 0, 0, None, None) == NULL
-    assert L.attn_prompt_weights(batch(), rows(), rows(), FAKE, -1, 0, FAKE, None) == SHAPE
-    assert L.attn_prompt_weights(batch(), rows(), rows(), FAKE, 0, 2, FAKE, None) == VALUE
+    assert L.attn_prompt(None, rows(), rows(), rows(), FAKE, None, FAKE, 1 << 40, None) == NULL
+    assert L.attn_prompt(batch(), None, rows(), rows(), FAKE, None, FAKE, 1 << 40, None) == NULL
+    assert prompt(L, out=None) == NULL and prompt(L, ws=None) == NULL
+    assert prompt(L, out=FAKE + 2) == ALIGN and prompt(L, lse=FAKE + 2) == ALIGN and prompt(L, ws=FAKE + 8) == ALIGN
+    assert gather(L, lse=None) == NULL and gather(L, out=None) == NULL and gather(L, ws=None) == NULL
+    assert gather(L, ws=FAKE + 8) == ALIGN and gather(L, last=-1) == SHAPE and gather(L, accumulate=2) == VALUE
+
+
+def test_prompt_workspace(L):
+    """Few rows against many keys need one; what is refused sizes to 0."""
+    b = batch(total_q=100, total_k=5000, n_seqs=1)
+    need = L.attn_prompt_workspace_size(b)
+    assert need > 0 and prompt(L, b, n=need - 1) == WORKSPACE and prompt(L, b, ws=None, n=0) == WORKSPACE
+    assert L.attn_prompt_workspace_size(batch(total_q=100000, total_k=100000)) == 0
+    assert L.attn_prompt_workspace_size(batch(total_q=100, total_k=5000, cu_q=None, cu_k=None, n_seqs=1)) == need
+    assert L.attn_prompt_workspace_size(batch(head_dim=80)) == 0 and L.attn_prompt_workspace_size(None) == 0
+    b = batch(total_q=5000, total_k=100, n_seqs=1)
+    need = L.attn_prompt_weights_workspace_size(b, 0)
+    assert need > 0 and gather(L, b, n=need - 1) == WORKSPACE
+    assert L.attn_prompt_weights_workspace_size(b, -1) == 0
+    assert L.attn_prompt_weights_workspace_size(batch(total_q=5000, total_k=10**6), 0) == 0
 
 
 def test_nothing_to_do_touches_no_device(L):
-    assert L.attn_prompt(batch(total_q=0), rows(None), rows(), rows(), None, None, None) == OK
-    assert L.attn_prompt_weights(batch(total_k=0), rows(), rows(None), FAKE, 0, 0, None, None) == OK
+    assert L.attn_prompt(batch(total_q=0), rows(None), rows(), rows(), None, None, None, 0, None) == OK
+    assert L.attn_prompt_weights(batch(total_k=0), rows(), rows(None), FAKE, 0, 0, None, None, 0, None) == OK
     assert L.kv4_append(cache(), seqs(), rows(), rows(), 1, 0, FAKE, None, None, None) == OK
     assert L.kv4_read(cache(), seqs(), FAKE, 0, 1, None, None, None) == OK
     assert L.kv4_attend(cache(), seqs(n_seqs=0), rows(), 1, 4, 1.0, 64, 0, None, None, None, 0, None) == OK
