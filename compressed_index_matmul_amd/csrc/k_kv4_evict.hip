@@ -18,11 +18,9 @@ namespace vqmm {
 
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWaves = kSelThreads / kWave;
 constexpr int kMoveThreads = 256;
-constexpr int kMovesPerBlock = kMoveThreads / kWave;
-constexpr int kFuseMoves = 16;  // at most one a wave of the selecting workgroup
+constexpr int kMovesPerBlock = kMoveThreads / 16;
+constexpr int kFuseMoves = 16;  // one for each 16 lanes of the smallest selecting workgroup
 
 // Keys in the order of the weights: NaN lowest, the protected slots on top.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -41,10 +39,11 @@ __device__ __forceinline__ int wave_prefix(int *s, int wave, int count) {
   return before;
 }
 
-// Copies slot src to slot dst, by one wave: keys and steps of both kinds,
-// weight and position.
+// Copies slot src to slot dst, by the 16 lanes l of one move: keys and values
+// with their steps and minima, weight and position.
+constexpr int kMoveLanes = 16;
 template <int D>
-__device__ __forceinline__ void move_slot(const KvView &c, int b, int kvh, int src, int dst, int lane) {
+__device__ __forceinline__ void move_slot(const KvView &c, int b, int kvh, int src, int dst, int l) {
   constexpr int DG = D / 32;
   const int64_t code_head = (int64_t)c.ps * (D / 2), scale_head = (int64_t)c.ps * (DG * 2);
   const int sp = src / c.ps, dp = dst / c.ps;
@@ -52,39 +51,47 @@ __device__ __forceinline__ void move_slot(const KvView &c, int b, int kvh, int s
   const int64_t spage = page_of(c, b, sp), dpage = page_of(c, b, dp);
   const uint8_t *sc = c.codes + (spage * 2 * c.hkv + kvh) * code_head;
   uint8_t *dc = c.codes + (dpage * 2 * c.hkv + kvh) * code_head;
-  const uint16_t *ss = c.scales + (spage * 2 * c.hkv + kvh) * scale_head;
-  uint16_t *ds = c.scales + (dpage * 2 * c.hkv + kvh) * scale_head;
+  const uint16_t *ss = c.scales + (spage * 2 * c.hkv + kvh) * scale_head + (so >> 2) * (DG * 8) + (so & 3);
+  uint16_t *ds = c.scales + (dpage * 2 * c.hkv + kvh) * scale_head + (d_o >> 2) * (DG * 8) + (d_o & 3);
   const int64_t sa = (spage * c.hkv + kvh) * c.ps + so, da = (dpage * c.hkv + kvh) * c.ps + d_o;
   const int sb = (so & 3) == 1 ? 2 : (so & 3) == 2 ? 1 : so & 3, db = (d_o & 3) == 1 ? 2 : (d_o & 3) == 2 ? 1 : d_o & 3;
+  const uint32_t *sk = reinterpret_cast<const uint32_t *>(sc + so * (D / 2));
+  uint32_t *dk = reinterpret_cast<uint32_t *>(dc + d_o * (D / 2));
   const uint8_t *sv = sc + c.hkv * code_head + (so >> 2) * (2 * D) + sb;
   uint8_t *dv = dc + c.hkv * code_head + (d_o >> 2) * (2 * D) + db;
-  constexpr int NV = (D / 2 + kWave - 1) / kWave;
+  constexpr int NK = (D / 8 + kMoveLanes - 1) / kMoveLanes, NV = D / 2 / kMoveLanes, NS = (4 * DG + kMoveLanes - 1) / kMoveLanes;
   // every load first: their latencies overlap
-  uint32_t key = 0;
-  uint16_t sm = 0;
-  uint8_t val[NV] = {};
-  float w = 0.0f;
-  int32_t at = 0;
-  const int kind = lane / (2 * DG), gs = lane % (2 * DG);  // (kind, group, step or minimum)
-  const int64_t k0 = kind * c.hkv * scale_head + gs * 4;
-  if (lane < D / 8) key = reinterpret_cast<const uint32_t *>(sc + so * (D / 2))[lane];
+  uint32_t key[NK] = {};
+  uint16_t sm[NS] = {};
+  uint8_t val[NV];
 #pragma unroll
-  for (int x = 0; x < NV; ++x)
-    if (x * kWave + lane < D / 2) val[x] = sv[(x * kWave + lane) * 4];
-  if (lane < 4 * DG) sm = ss[k0 + (so >> 2) * (DG * 8) + (so & 3)];
-  if (lane == 62) w = c.weights[sa];
-  if (lane == 63) at = c.pos[sa];
-  if (lane < D / 8) reinterpret_cast<uint32_t *>(dc + d_o * (D / 2))[lane] = key;
+  for (int x = 0; x < NK; ++x)
+    if (x * kMoveLanes + l < D / 8) key[x] = sk[x * kMoveLanes + l];
 #pragma unroll
-  for (int x = 0; x < NV; ++x)
-    if (x * kWave + lane < D / 2) dv[(x * kWave + lane) * 4] = val[x];
-  if (lane < 4 * DG) ds[k0 + (d_o >> 2) * (DG * 8) + (d_o & 3)] = sm;
-  if (lane == 62) c.weights[da] = w;
-  if (lane == 63) c.pos[da] = at;
+  for (int x = 0; x < NV; ++x) val[x] = sv[(x * kMoveLanes + l) * 4];
+#pragma unroll
+  for (int x = 0; x < NS; ++x) {  // (kind, group, step or minimum)
+    const int i = x * kMoveLanes + l;
+    if (i < 4 * DG) sm[x] = ss[i / (2 * DG) * (c.hkv * scale_head) + i % (2 * DG) * 4];
+  }
+  const float w = c.weights[sa];
+  const int32_t at = c.pos[sa];
+#pragma unroll
+  for (int x = 0; x < NK; ++x)
+    if (x * kMoveLanes + l < D / 8) dk[x * kMoveLanes + l] = key[x];
+#pragma unroll
+  for (int x = 0; x < NV; ++x) dv[(x * kMoveLanes + l) * 4] = val[x];
+#pragma unroll
+  for (int x = 0; x < NS; ++x) {
+    const int i = x * kMoveLanes + l;
+    if (i < 4 * DG) ds[i / (2 * DG) * (c.hkv * scale_head) + i % (2 * DG) * 4] = sm[x];
+  }
+  if (l == 0) c.weights[da] = w;
+  if (l == 1) c.pos[da] = at;
 }
 
 // A wave's run of slots, 64 at a time, and where their keys are kept: in
-// registers (R > 0: up to 1024 R slots) or in the workspace (R = 0).
+// registers (R > 0: up to R a thread) or in the workspace (R = 0).
 template <int R>
 struct Keys {
   uint32_t r[R];
@@ -111,11 +118,13 @@ __device__ __forceinline__ void each_step(int steps, int first, F f) {
 
 constexpr int kCopies = 4;  // histograms of a wave: equal digits of neighbouring lanes fall on different counters
 
-// FUSE > 0: the workgroup moves its few slots itself, head_dim FUSE.
-template <int R, int FUSE>
-__global__ __launch_bounds__(kSelThreads) void k_kv4_select(KvView c, EvictPlan p, const int32_t *__restrict__ next_pos,
+// NT threads a row.  FUSE > 0: the workgroup moves its few slots itself,
+// head_dim FUSE.
+template <int NT, int R, int FUSE>
+__global__ __launch_bounds__(NT) void k_kv4_select(KvView c, EvictPlan p, const int32_t *__restrict__ next_pos,
                                                             int keep, int recent, uint32_t *__restrict__ keys_all,
                                                             int32_t *__restrict__ moves, int32_t *__restrict__ counts) {
+  constexpr int kSelThreads = NT, kSelWaves = NT / kWave;
   __shared__ int s_hist[kSelWaves / 4][kCopies][256];
   __shared__ int s_sum[256];
   __shared__ int s_wave[kSelWaves];
@@ -136,19 +145,40 @@ __global__ __launch_bounds__(kSelThreads) void k_kv4_select(KvView c, EvictPlan 
   const int steps = (len + kSelThreads - 1) / kSelThreads;
   const int first = wave * steps * kWave + lane;
 
-  // Keys in the order of the weights, protected slots on top; lanes past the
-  // end hold 0 and count nowhere (a NaN's 0 does count: `slot < len` is asked).
+  // Keys in the order of the weights, protected slots on top; what lanes past
+  // the end hold counts nowhere.
   Keys<R> keys;
   const int tiles = c.ps / 32;
-  each_step<R>(steps, first, [&](int i, int slot) {
-    uint32_t key = 0;
-    if (slot < len) {
-      const int pi = (slot >> 5) / tiles;
-      const int64_t at = (page_of(c, b, pi) * c.hkv + kvh) * c.ps + (slot - pi * c.ps);
-      key = c.pos[at] >= oldest ? 0xffffffffu : weight_key(c.weights[at]);
+  constexpr int kBatch = 8;  // steps whose loads go out together
+  auto load = [&](int i0) {
+    int64_t at[kBatch];
+    int32_t pos[kBatch];
+    float w[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int slot = min(first + (i0 + j) * kWave, len - 1), pi = (slot >> 5) / tiles;
+      at[j] = (page_of(c, b, pi) * c.hkv + kvh) * c.ps + (slot - pi * c.ps);
     }
-    if (R > 0 || slot < len) keys.set(i, ws, slot, key);
-  });
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) pos[j] = c.pos[at[j]], w[j] = c.weights[at[j]];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int slot = first + (i0 + j) * kWave;
+      const uint32_t key = pos[j] >= oldest ? 0xffffffffu : weight_key(w[j]);
+      if (R > 0) {
+        if (i0 + j < R) keys.set(i0 + j, ws, slot, key);
+      } else if (i0 + j < steps && slot < len) {
+        keys.set(i0 + j, ws, slot, key);
+      }
+    }
+  };
+  if (R > 0) {
+#pragma unroll
+    for (int i0 = 0; i0 < R; i0 += kBatch)
+      if (i0 < steps) load(i0);
+  } else {
+    for (int i0 = 0; i0 < steps; i0 += kBatch) load(i0);
+  }
 
   uint32_t prefix = 0;
   int need = keep;
@@ -234,7 +264,8 @@ __global__ __launch_bounds__(kSelThreads) void k_kv4_select(KvView c, EvictPlan 
   }
   if (FUSE) {
     __syncthreads();
-    for (int i = wave; i < s_need; i += kSelWaves) move_slot<FUSE ? FUSE : 64>(c, b, kvh, s_from[i], s_to[i], lane);
+    const int i = tid / kMoveLanes;
+    if (i < s_need) move_slot<FUSE ? FUSE : 64>(c, b, kvh, s_from[i], s_to[i], lane % kMoveLanes);
   }
 }
 
@@ -242,30 +273,33 @@ template <int D>
 __global__ __launch_bounds__(kMoveThreads) void k_kv4_move(KvView c, EvictPlan p, const int32_t *__restrict__ moves,
                                                            const int32_t *__restrict__ counts, int chunks) {
   const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
-  const int i = chunk * kMovesPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = chunk * kMovesPerBlock + threadIdx.x / kMoveLanes;
   if (i >= counts[row]) return;
   const int32_t *to = moves + (int64_t)row * 2 * p.max_moves, *from = to + p.max_moves;
-  move_slot<D>(c, row / c.hkv, row % c.hkv, from[i], to[i], threadIdx.x & 63);
+  move_slot<D>(c, row / c.hkv, row % c.hkv, from[i], to[i], threadIdx.x % kMoveLanes);
 }
 
-template <int R, int FUSE>
+template <int NT, int R, int FUSE>
 hipError_t select_rows(const KvView &c, const EvictPlan &p, const int32_t *next_pos, int keep, int recent, uint32_t *keys,
                        int32_t *moves, int32_t *counts, hipStream_t s) {
-  k_kv4_select<R, FUSE><<<c.nseq * c.hkv, kSelThreads, 0, s>>>(c, p, next_pos, keep, recent, keys, moves, counts);
+  k_kv4_select<NT, R, FUSE><<<c.nseq * c.hkv, NT, 0, s>>>(c, p, next_pos, keep, recent, keys, moves, counts);
   return hipGetLastError();
 }
 
+// Rows of up to 2048 slots take four waves (barriers are cheaper there), up
+// to 32768 sixteen; longer ones keep their keys in the workspace.
 template <int D>
 hipError_t evict_d(const KvView &c, const EvictPlan &p, const int32_t *next_pos, int keep, int recent, uint32_t *keys,
                    int32_t *moves, int32_t *counts, hipStream_t s) {
   const int rows = c.nseq * c.hkv;
   if (p.max_moves <= kFuseMoves) {
-    if (p.len_cap <= 2 * kSelThreads) return select_rows<2, D>(c, p, next_pos, keep, recent, keys, moves, counts, s);
-    if (p.len_cap <= 16 * kSelThreads) return select_rows<16, D>(c, p, next_pos, keep, recent, keys, moves, counts, s);
+    if (p.len_cap <= 2048) return select_rows<256, 8, D>(c, p, next_pos, keep, recent, keys, moves, counts, s);
+    if (p.len_cap <= 16384) return select_rows<1024, 16, D>(c, p, next_pos, keep, recent, keys, moves, counts, s);
   }
-  hipError_t e = p.len_cap <= 16 * kSelThreads   ? select_rows<16, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
-                 : p.len_cap <= 32 * kSelThreads ? select_rows<32, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
-                                                 : select_rows<0, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s);
+  hipError_t e = p.len_cap <= 2048    ? select_rows<256, 8, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
+                 : p.len_cap <= 16384 ? select_rows<1024, 16, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
+                 : p.len_cap <= 32768 ? select_rows<1024, 32, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
+                                      : select_rows<1024, 0, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s);
   if (e != hipSuccess) return e;
   const int chunks = (p.max_moves + kMovesPerBlock - 1) / kMovesPerBlock;
   if ((int64_t)rows * chunks >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
