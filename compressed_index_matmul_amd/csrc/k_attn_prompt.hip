@@ -34,35 +34,98 @@ __device__ __forceinline__ float16_t mfma32(uint4_t a, uint4_t b, float16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
+// LDS by byte address.
+typedef __attribute__((address_space(3))) uint4_t lds_uint4;
+typedef __attribute__((address_space(3))) short4_t lds_short4;
+__device__ __forceinline__ uint4_t lds_read(uint32_t at) { return *(lds_uint4 *)at; }
 // Four 16-bit values of one column, rows 0..3 of a 4 x 16 block in LDS whose
 // row r, columns 4 j .. 4 j + 3 the lane 4 r + j of the 16 points at.
-__device__ __forceinline__ uint2_t lds_column(const uint16_t *p) {
-  typedef __attribute__((address_space(3))) short4_t lds_short4;
-  return __builtin_bit_cast(uint2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)p));
+__device__ __forceinline__ uint2_t lds_column(uint32_t at) {
+  return __builtin_bit_cast(uint2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)at));
 }
 
-// BN rows of D channels of one head into registers (rows >= n: zeros), then
-// into LDS.
-template <int D, int BN, int PAD>
+// Tiles of BN rows go from global memory straight into LDS, 16 bytes a lane, a
+// wave's 64 pieces next to one another: no registers, no LDS writes to issue.
+// Rows are not padded; instead the 16-byte pieces of a row are permuted by an
+// XOR with bits of the row, in the address each lane loads from:
+//   keys   : piece ^ (row & 15) (D = 64: row / 2 & 7): 16 rows of one piece,
+//            a quarter of a b128 read
+//   values : piece ^ 4 (row & 3) (D = 64: 4 (row / 2 & 1)): the 64-byte spans
+//            that the transposing reads take from 4 rows
+// fall on different banks (64 of 4 bytes).
+template <int D>
+__device__ __forceinline__ int key_swizzle(int row) {
+  return D == 64 ? (row >> 1) & 7 : row & 15;
+}
+template <int D>
+__device__ __forceinline__ int value_swizzle(int row) {
+  return D == 64 ? (row & 2) << 1 : (row & 3) << 2;
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+
+// 16 bytes a lane from base + off to LDS at `lds` + 16 lane (m0; nothing else here
+// uses it).  Not waited for:
+// wait_loads() before the barrier that publishes the tile.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, const char *base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <int D, int BN>
 struct Stage {
-  static constexpr int kPieces = BN * (D / 8) / kThreads;
-  uint4_t r[kPieces];
-  __device__ __forceinline__ void load(const uint16_t *base, int64_t ts, int row0, int n) {
+  static constexpr int kRowsPerLoad = 512 / D;                    // rows of a wave's 1024 bytes
+  static constexpr int kLoads = BN / (4 * kRowsPerLoad);          // of a wave and tile
+  // the lane's row of the tile for the wave's first load, and its piece in the
+  // even and in the odd loads (4 kRowsPerLoad rows apart)
+  uint32_t row, piece[2];
+  __device__ __forceinline__ Stage(int wave, int lane, bool value) {
+    row = kRowsPerLoad * wave + lane / (D / 8);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int id = threadIdx.x + i * kThreads, row = row0 + id / (D / 8), col = id % (D / 8) * 8;
-      r[i] = uint4_t{0, 0, 0, 0};
-      if (row < n) r[i] = *reinterpret_cast<const uint4_t *>(base + row * ts + col);
+    for (int i = 0; i < 2; ++i) {
+      const int r = row + i * 4 * kRowsPerLoad;
+      piece[i] = (lane % (D / 8)) ^ (value ? value_swizzle<D>(r) : key_swizzle<D>(r));
     }
   }
-  __device__ __forceinline__ void store(uint16_t *s) const {
+  // rows row0 .. row0 + BN - 1 of n (those past the end repeat the last one)
+  __device__ __forceinline__ void load(uint32_t lds, const uint16_t *base, int64_t ts, int row0, int n, int wave) const {
+    lds += wave * 1024;
+    const char *p = reinterpret_cast<const char *>(base + row0 * ts);
+    if (row0 + BN <= n) {
+      const uint32_t off = row * (uint32_t)ts * 2u;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int id = threadIdx.x + i * kThreads;
-      *reinterpret_cast<uint4_t *>(s + (id / (D / 8)) * (D + PAD) + id % (D / 8) * 8) = r[i];
+      for (int i = 0; i < kLoads; ++i)
+        load_to_lds(lds + i * 4096, p + (int64_t)i * (4 * kRowsPerLoad) * ts * 2, off + piece[i & 1] * 16u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        load_to_lds(lds + i * 4096, p, (uint32_t)min((int)row + i * 4 * kRowsPerLoad, n - 1 - row0) * (uint32_t)ts * 2u + piece[i & 1] * 16u);
     }
   }
 };
+
+// Infinities and NaN among the eight values of a 16-byte piece become zeros;
+// returns whether there were any.
+template <bool F16>
+__device__ __forceinline__ bool clear_nonfinite(uint4_t &w) {
+  constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u, kOne = F16 ? 0x04000400u : 0x00800080u;
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t full = ((w[i] & kExp) + kOne) & 0x80008000u;  // a full exponent carries into the sign's place
+    any |= full;
+    w[i] &= ~((full >> 15) * 0xffffu);
+  }
+  return any != 0;
+}
+template <bool F16>
+__device__ __forceinline__ float nonfinite_of(uint32_t h) {
+  const float f = F16 ? h2f(h) : bf2f(h);
+  return __builtin_isfinite(f) ? 0.0f : f;
+}
 
 // The pieces of a row block's keys: `piece` of them takes tiles from *lo to
 // *hi of nt, none shorter than kMinTiles but the last.
@@ -83,12 +146,12 @@ struct PromptOut {
 // SPLIT: the workgroup takes one piece of its keys and leaves its sums in the
 // workspace for k_attn_join.
 template <int D, int BN, bool F16, bool CAUSAL, bool SPLIT>
-__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(AttnView a, PromptOut o, int tiles,
+__global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 1) void k_attn_prompt(AttnView a, PromptOut o, int tiles,
                                                                             int pieces) {
-  constexpr int KP = 8, VP = 32;  // padding of an LDS row, in elements
   constexpr int NS = BN / 32, ND = D / 32, NK = D / 16;
-  __shared__ __attribute__((aligned(16))) uint16_t s_k[2][BN * (D + KP)];
-  __shared__ __attribute__((aligned(16))) uint16_t s_v[2][BN * (D + VP)];
+  __shared__ __attribute__((aligned(1024))) uint16_t s_k[2][BN * D];
+  __shared__ __attribute__((aligned(1024))) uint16_t s_v[2][BN * D];
+  __shared__ int s_cleared;
 
   // heads of a group share keys and values: they come next to one another,
   // key/value heads fastest (workgroups are dealt to the XCDs in turn, so with
@@ -119,6 +182,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(Attn
   const int lim = CAUSAL ? min(qi + off, rk.n - 1) : rk.n - 1;  // last key this lane's query sees
   const int lim_first = CAUSAL ? min(qw + off, rk.n - 1) : rk.n - 1, lim_last = CAUSAL ? min(qw + 31 + off, rk.n - 1) : rk.n - 1;
   const int seen = CAUSAL ? min(q0 + kRows + off, rk.n) : rk.n;  // keys the workgroup needs
+  const int all_see = CAUSAL ? min(q0 + off, rk.n - 1) : rk.n - 1;  // the last key that every query of it sees
   int t_lo = 0, nt = seen > 0 ? (seen + BN - 1) / BN : 0;
   if (SPLIT) {
     piece_tiles(nt, pieces, piece, BN, &t_lo, &nt);
@@ -143,32 +207,63 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(Attn
   const float cs = a.scale * kLog2e;
   const float slack = kSlack / cs;
 
-  Stage<D, BN, KP> sk;
-  Stage<D, BN, VP> sv;
-  if (t_lo < nt) {
-    sk.load(kb, a.k_ts, t_lo * BN, seen);
-    sv.load(vb, a.v_ts, t_lo * BN, seen);
-    sk.store(s_k[t_lo & 1]);
-    sv.store(s_v[t_lo & 1]);
-  }
+  const Stage<D, BN> sk(wave, lane, false), sv(wave, lane, true);
+  const uint32_t lk = lds_address(s_k), lv = lds_address(s_v);
+  auto fetch = [&](int t) {
+    sk.load(lk + (t & 1) * (BN * D * 2), kb, a.k_ts, t * BN, seen, wave);
+    sv.load(lv + (t & 1) * (BN * D * 2), vb, a.v_ts, t * BN, seen, wave);
+  };
+  // Where the lane reads: piece 2 i + h of its key row, at ka ^ 32 i (256 bytes on from i = 8); of the value rows
+  // 4 h + (i16 / 4) the channels 16 (lane / 16 % 2) + 4 (i16 % 4) of 32-channel block d, at va ^ 64 d (256 bytes on
+  // from d = 4).  The swizzles are XORs too, and rows and tiles begin at multiples of 128 or 256 bytes, so one base a
+  // tile does.
+  const uint32_t ka = lk + col * (2 * D) + (h ^ key_swizzle<D>(col)) * 16;
+  const int vrow = 4 * h + ((lane & 15) >> 2);
+  const uint32_t va = lv + vrow * (2 * D) + ((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swizzle<D>(vrow)) * 16 + (lane & 1) * 8;
+  if (threadIdx.x == 0) s_cleared = 0;
+  if (t_lo < nt) fetch(t_lo);
+  wait_loads();
   __syncthreads();
   for (int t = t_lo; t < nt; ++t) {
     const int k0 = t * BN;
-    if (t + 1 < nt) {
-      sk.load(kb, a.k_ts, k0 + BN, seen);
-      sv.load(vb, a.v_ts, k0 + BN, seen);
+    if (t + 1 < nt) fetch(t + 1);
+    if (k0 + BN - 1 > all_see) {
+      // Some query does not see some key of this tile: its probability is 0, but 0 times an infinity would be NaN.
+      // What is not finite leaves the tile and comes back at the end, for the queries that do see it.
+#pragma unroll
+      for (int i = threadIdx.x; i < BN * D / 8; i += kThreads) {
+        uint4_t *p = reinterpret_cast<uint4_t *>(s_v[t & 1]) + i;
+        uint4_t w = *p;
+        if (clear_nonfinite<F16>(w)) {
+          *p = w;
+          s_cleared = 1;
+        }
+      }
+      __syncthreads();
     }
     if (k0 <= lim_last) {
-      const uint16_t *ks = s_k[t & 1] + col * (D + KP) + 8 * h;
+      const uint32_t ks = ka + (t & 1) * (BN * D * 2), vs = va + (t & 1) * (BN * D * 2);
       float16_t S[NS];
+      uint4_t kf[2][NK];
+#pragma unroll
+      for (int i = 0; i < NK; ++i) kf[0][i] = lds_read((ks ^ (i & 7) * 32) + (i >> 3) * 256);
+      sched_fence();
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) S[n][r] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NK; ++i)
-          S[n] = mfma32<F16>(*reinterpret_cast<const uint4_t *>(ks + n * 32 * (D + KP) + 16 * i), qf[i], S[n]);
+        for (int i = 0; i < NK; ++i) {
+          if (n + 1 < NS) kf[(n + 1) & 1][i] = lds_read((ks ^ (i & 7) * 32) + (n + 1) * 64 * D + (i >> 3) * 256);
+          S[n] = mfma32<F16>(kf[n & 1][i], qf[i], S[n]);
+        }
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+          if (n + 1 < NS) sched_group<0x100, 1>();
+          sched_group<0x008, 1>();
+        }
       }
+      sched_fence();
       if (k0 + BN - 1 > lim_first) {
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -202,28 +297,56 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_attn_prompt(Attn
           part[r & 3] += S[n][r];
         }
       lsum += (part[0] + part[1]) + (part[2] + part[3]);
-      // V^T: rows 4 h + (i16 / 4), columns 16 (lane / 16 % 2) + 4 (i16 % 4) of each 8-key, 32-channel block
-      const uint16_t *vs = s_v[t & 1] + (4 * h + ((lane & 15) >> 2)) * (D + VP) + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+      uint4_t vf[2][ND];
+      auto read_v = [&](uint4_t *v, int st) {
 #pragma unroll
-      for (int n = 0; n < NS; ++n)
+        for (int d = 0; d < ND; ++d) {
+          const uint32_t p = (vs ^ (d & 3) * 64) + 32 * st * D + (d >> 2) * 256;
+          const uint2_t v0 = lds_column(p), v1 = lds_column(p + 16 * D);
+          v[d] = uint4_t{v0[0], v0[1], v1[0], v1[1]};
+        }
+      };
+      read_v(vf[0], 0);
+      uint4_t pf[2 * NS];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint4_t pf;
+      for (int st = 0; st < 2 * NS; ++st)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pf[i] = pack16<F16>(S[n][8 * x + 2 * i], S[n][8 * x + 2 * i + 1]);
+        for (int i = 0; i < 4; ++i) pf[st][i] = pack16<F16>(S[st / 2][8 * (st & 1) + 2 * i], S[st / 2][8 * (st & 1) + 2 * i + 1]);
+      sched_fence();
 #pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            const uint16_t *vp = vs + (32 * n + 16 * x) * (D + VP) + 32 * d;
-            const uint2_t v0 = lds_column(vp), v1 = lds_column(vp + 8 * (D + VP));
-            acc[d] = mfma32<F16>(uint4_t{v0[0], v0[1], v1[0], v1[1]}, pf, acc[d]);
+      for (int st = 0; st < 2 * NS; ++st) {
+        if (st + 1 < 2 * NS) read_v(vf[(st + 1) & 1], st + 1);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[d] = mfma32<F16>(vf[st & 1][d], pf[st], acc[d]);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          if (st + 1 < 2 * NS) sched_group<0x100, 2>();
+          sched_group<0x008, 1>();
+        }
+      }
+      sched_fence();
+    }
+    wait_loads();
+    __syncthreads();
+  }
+
+  if (s_cleared) {
+#pragma unroll 1
+    for (int key = max((all_see + 1) / BN * BN, t_lo * BN); key < min(seen, nt * BN); ++key) {
+      const uint16_t *vp_key = vb + key * a.v_ts + 4 * h;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint2_t w = *reinterpret_cast<const uint2_t *>(vp_key + 32 * d + 8 * x);
+          if (key <= lim) {
+            acc[d][4 * x] += nonfinite_of<F16>(w[0] & 0xffffu);
+            acc[d][4 * x + 1] += nonfinite_of<F16>(w[0] >> 16);
+            acc[d][4 * x + 2] += nonfinite_of<F16>(w[1] & 0xffffu);
+            acc[d][4 * x + 3] += nonfinite_of<F16>(w[1] >> 16);
           }
         }
     }
-    if (t + 1 < nt) {
-      sk.store(s_k[(t + 1) & 1]);
-      sv.store(s_v[(t + 1) & 1]);
-    }
-    __syncthreads();
   }
 
   lsum = sum_xor32(lsum);
@@ -344,7 +467,7 @@ hipError_t launch_attn_prompt(const AttnView &a, const PromptPlan &p, uint16_t *
   char *w = static_cast<char *>(ws);
   const PromptOut o{out, lse, reinterpret_cast<float *>(w), reinterpret_cast<float *>(w + p.stat_off)};
   if (a.d == 64) return a.f16 ? prompt_d<64, 64, true>(a, p, o, s) : prompt_d<64, 64, false>(a, p, o, s);
-  if (a.d == 128) return a.f16 ? prompt_d<128, 64, true>(a, p, o, s) : prompt_d<128, 64, false>(a, p, o, s);
+  if (a.d == 128) return a.f16 ? prompt_d<128, 32, true>(a, p, o, s) : prompt_d<128, 32, false>(a, p, o, s);
   return a.f16 ? prompt_d<256, 32, true>(a, p, o, s) : prompt_d<256, 32, false>(a, p, o, s);
 }
 

@@ -142,6 +142,41 @@ def test_other_rows_do_not_reach_a_sequence(vq, d, bad):
         assert torch.equal(w[:, rows], wref[:, rows])
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_masked_places_hold_anything(vq, d, kind, bad):
+    """A non-finite value or key reaches the queries that see it and no other,
+    within the same tile too; the channels beside it stay as they were."""
+    import torch
+    rng = np.random.default_rng(d)
+    n, keys = 150, (149, 77, 64, 40, 5)
+    cu, cu_d = offsets([n])
+    q, _ = heads(rng, n, 2, d, kind)
+    k, _ = heads(rng, n, 1, d, kind)
+    v, _ = heads(rng, n, 1, d, kind)
+    want, lse = vq.attn_prompt(q, k, v, cu_d, return_lse=True)
+    wref = vq.attn_prompt_weights(q, k, lse, cu_d)
+    for j in keys:
+        v2 = v.clone()
+        v2[j, 0, 3] = v2[j, 0, d - 1] = bad
+        got, l2 = vq.attn_prompt(q, k, v2, cu_d, return_lse=True)
+        assert torch.equal(l2, lse)
+        assert torch.equal(got[:j], want[:j]), j
+        others = torch.ones(d, dtype=torch.bool, device="cuda")
+        others[3] = others[d - 1] = False
+        assert torch.equal(got[j:, :, others], want[j:, :, others]), j
+        hit = got[j:, :, ~others].float()
+        assert bool((torch.isnan(hit) if bad != bad else hit == bad).all()), j
+        k2 = k.clone()
+        k2[j] = bad
+        got, l2 = vq.attn_prompt(q, k2, v, cu_d, return_lse=True)
+        assert torch.equal(got[:j], want[:j]) and torch.equal(l2[:, :j], lse[:, :j]), j
+        if j == n - 1:  # the weights of the keys before it, over the queries before it
+            w = vq.attn_prompt_weights(q[:j], k2[:j], lse[:, :j].contiguous(), ints([0, j]))
+            assert bool(torch.isfinite(w).all())
+
+
 def test_weights_accumulate_and_sum(vq):
     import torch
     rng = np.random.default_rng(8)
