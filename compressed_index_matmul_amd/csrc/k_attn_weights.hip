@@ -166,14 +166,15 @@ hipError_t weights_d(const AttnView &a, const PromptPlan &p, const float *lse, i
 
 }  // namespace
 
-// Few key blocks (less than two a CU) are cut along the queries, into at
-// most 16 pieces of at least one tile.
+// Few key blocks (less than one and a half a CU) are cut along the queries,
+// into about 1536 workgroups of at least one tile: under a causal mask the
+// first keys have the most queries, so pieces also even the work out.
 PromptPlan attn_weights_plan(const AttnView &a, int last) {
   PromptPlan p{1, 0, 0};
   const int64_t blocks = ((int64_t)a.tk / kKeys + a.nseq) * a.hkv;
   const int64_t queries = last > 0 ? std::min(last, a.tq) : a.tq;
   const int64_t most = (queries + 63) / 64 * (a.hq / a.hkv);
-  if (blocks > 0 && blocks < 512 && most > 1) p.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({512 / blocks, most, 16}));
+  if (blocks > 0 && blocks < 384 && most > 1) p.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({1536 / blocks, most, 32}));
   if (p.pieces > 1) p.bytes = (size_t)p.pieces * a.hkv * a.tk * 4;
   return p;
 }

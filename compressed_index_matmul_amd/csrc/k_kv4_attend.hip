@@ -28,8 +28,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
+constexpr int kLoneWaves = 8;  // of a workgroup that takes a whole sequence and head
 constexpr int kTile = 32;  // slots a wave takes at a time
 constexpr int kPieces = 3072;
+constexpr int kLoneSlots = 1024;
 constexpr float kSlack = 8.0f;  // the reference maximum lags by up to 2^8: p <= 256 is in fp16's range
 
 // dword N of the 16 lanes of a row, in all of them.
@@ -141,8 +143,9 @@ struct AttendArgs {
   float *score;  // [seq][head][pitch], log2 domain
 };
 
-template <int D, bool F16, bool WEIGH>
-__global__ __launch_bounds__(kThreads, 2) void k_kv4_attend(KvView c, AttendPlan p, AttendArgs a) {
+template <int D, bool F16, bool WEIGH, int NW>
+__global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPlan p, AttendArgs a) {
+  constexpr int kThreads = NW * kWave, kWaves = NW;
   constexpr int DG = D / 32, CH = D / 16;
   constexpr int kPitch = D + 4;  // floats of a head's row in LDS: 16-byte pieces of 16 rows fall on different banks
   __shared__ float s_o[kWaves][16][kPitch];
@@ -414,6 +417,7 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
     }
     __syncthreads();
     if (slot < len)
+#pragma unroll 8
       for (int g = 0; g < ng; ++g) {
         const float4_t x = *reinterpret_cast<const float4_t *>(a.score + (row0 + g) * p.score_pitch + slot);
 #pragma unroll
@@ -436,8 +440,9 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
 template <int D, bool F16>
 hipError_t attend_d(const KvView &c, const AttendPlan &p, const AttendArgs &a, bool weigh, hipStream_t s) {
   const unsigned blocks = (unsigned)((int64_t)c.nseq * c.hkv * p.htiles * p.splits);
-  if (weigh) k_kv4_attend<D, F16, true><<<blocks, kThreads, 0, s>>>(c, p, a);
-  else k_kv4_attend<D, F16, false><<<blocks, kThreads, 0, s>>>(c, p, a);
+  if (weigh) k_kv4_attend<D, F16, true, kWaves><<<blocks, kThreads, 0, s>>>(c, p, a);
+  else if (p.lone) k_kv4_attend<D, F16, false, kLoneWaves><<<blocks, kLoneWaves * kWave, 0, s>>>(c, p, a);
+  else k_kv4_attend<D, F16, false, kWaves><<<blocks, kThreads, 0, s>>>(c, p, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (p.splits == 1 && !weigh)) return e;
   const int out_blocks = p.splits > 1 ? c.nseq * a.hq : 0;
@@ -464,6 +469,8 @@ AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add
   const int64_t rounds = std::max<int64_t>(1, ((int64_t)p.len_cap * work + kPieces * round_slots - 1) / (kPieces * round_slots));
   p.tiles = (int)std::min<int64_t>(rounds * kWaves, ((int64_t)1 << 26));
   p.splits = (int)std::max<int64_t>(1, ((int64_t)p.len_cap + p.tiles * kTile - 1) / ((int64_t)p.tiles * kTile));
+  p.lone = !add_weights && p.splits > 1 && p.len_cap <= kLoneSlots && work <= 256;
+  if (p.lone) p.splits = 1, p.tiles = (p.len_cap + kTile - 1) / kTile;
   p.score_pitch = (p.len_cap + kTile - 1) / kTile * kTile;
   const size_t rows = (size_t)c.nseq * n_q_heads;
   auto round = [](size_t x) { return (x + 255) & ~(size_t)255; };

@@ -21,18 +21,18 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Largest / smallest over the four lanes of a quad; NaN wins either way.
-__device__ __forceinline__ float quad_pick(float v, bool want_max) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int u = __float_as_int(v);
-    const int w = i == 0 ? __builtin_amdgcn_update_dpp(u, u, 0xB1, 0xF, 0xF, false)   // quad_perm 1,0,3,2
-                         : __builtin_amdgcn_update_dpp(u, u, 0x4E, 0xF, 0xF, false);  // quad_perm 2,3,0,1
-    const float o = __int_as_float(w);
-    if (want_max) v = (o > v || o != o) ? o : v;
-    else v = (o < v || o != o) ? o : v;
-  }
-  return v;
+// Smallest / largest, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) { return __builtin_elementwise_minimum(a, b); }
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+// The lane's neighbours in its four: lane ^ 1, lane ^ 2.
+__device__ __forceinline__ float quad_xor1(float v) {
+  const int u = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(u, u, 0xB1, 0xF, 0xF, false));  // quad_perm 1,0,3,2
+}
+__device__ __forceinline__ float quad_xor2(float v) {
+  const int u = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(u, u, 0x4E, 0xF, 0xF, false));  // quad_perm 2,3,0,1
 }
 
 template <int DT>
@@ -162,19 +162,13 @@ __global__ __launch_bounds__(kThreads) void k_kv4_append(KvView c, const void *_
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = 0.0f;
     }
-    float lo = 0.0f, hi = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float xx = x[j];
-      x[j] = xx != xx ? xx : fminf(fmaxf(xx, -32768.0f), 32768.0f);
-      if (j == 0) lo = hi = x[0];
-      else {
-        lo = (x[j] < lo || x[j] != x[j]) ? x[j] : lo;
-        hi = (x[j] > hi || x[j] != x[j]) ? x[j] : hi;
-      }
-    }
-    lo = quad_pick(lo, false);
-    hi = quad_pick(hi, true);
+    float lo = min_nan(min_nan(min_nan(x[0], x[1]), min_nan(x[2], x[3])), min_nan(min_nan(x[4], x[5]), min_nan(x[6], x[7])));
+    float hi = max_nan(max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])), max_nan(max_nan(x[4], x[5]), max_nan(x[6], x[7])));
+    lo = min_nan(lo, quad_xor1(lo));
+    hi = max_nan(hi, quad_xor1(hi));
+    // Saturating the ends saturates every value: one beyond them gets the code of the end, 0 or 15.
+    lo = max_nan(min_nan(min_nan(lo, quad_xor2(lo)), 32768.0f), -32768.0f);
+    hi = max_nan(min_nan(max_nan(hi, quad_xor2(hi)), 32768.0f), -32768.0f);
     float step = (hi - lo) * (1.0f / 15.0f);
     asm("" : "+v"(step));  // rounded to fp32 first: a fused multiply and conversion would round once
     const _Float16 m = (_Float16)lo, s = (_Float16)step;
@@ -183,9 +177,8 @@ __global__ __launch_bounds__(kThreads) void k_kv4_append(KvView c, const void *_
     uint32_t w = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float t = (x[j] - mf) * r;  // NaN: the minimum below gives 0
-      const float q = fminf(fmaxf(__builtin_rintf(t), 0.0f), 15.0f);
-      w |= (uint32_t)q << (4 * j);
+      const float t = (x[j] - mf) * r;  // NaN: the median is the smaller bound
+      w |= (uint32_t)__builtin_rintf(__builtin_amdgcn_fmed3f(t, 0.0f, 15.0f)) << (4 * j);
     }
     word[i] = w;
     s16[i] = __builtin_bit_cast(uint16_t, s);

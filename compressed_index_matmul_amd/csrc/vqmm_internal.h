@@ -135,6 +135,7 @@ struct AttendPlan {
   int htiles;       // 16-head tiles of a group
   int tiles;        // 32-slot tiles of one piece of a sequence and head
   int splits;       // pieces that the longest sequence may have
+  bool lone;        // short: one workgroup of more waves takes it whole
   int len_cap;      // lengths are clamped to this
   int score_pitch;  // floats per head of stored scores (add_weights)
   size_t part_off, stat_off, score_off, bytes;

@@ -269,18 +269,36 @@ def test_attend_strided_queries_workspace_stream(vq):
     want, lse = vq.kv4_attend(q, cache, t, ints(lens), return_lse=True)
     wide = torch.full((3, 12, 128), float("nan"), dtype=q.dtype, device="cuda")
     wide[:, :8] = q
-    need = vq.kv4_attend_workspace_size(cache, 3, 8, 512, False)
-    assert need > 0
-    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((vq.kv4_attend_workspace_size(cache, 3, 8, 512, False) + 16,), 0xFF, dtype=torch.uint8, device="cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     out = torch.empty_like(want)
     got, l2 = vq.kv4_attend(wide[:, :8], cache, t, ints(lens), max_len=512, workspace=ws, out=out, return_lse=True, stream=side)
     side.synchronize()
     assert got.data_ptr() == out.data_ptr() and torch.equal(got, want) and torch.equal(l2, lse)
-    with pytest.raises(vq.VQError) as e:
-        vq.kv4_attend(q, cache, t, ints(lens), max_len=512, workspace=ws[:need - 16])
-    assert e.value.status == -8
+
+
+def test_attend_workspace(vq):
+    """A workspace of the asked size serves, whatever it holds; a smaller one
+    is refused; one for a longer bound does too."""
+    import torch
+    rng = np.random.default_rng(16)
+    lens = [3000, 20, 333]
+    cache, table, t = filled(vq, rng, lens, 2, 128, 64)
+    q, _ = heads(rng, 3, 8, 128, "bf16")
+    for weigh in (False, True):
+        need = vq.kv4_attend_workspace_size(cache, 3, 8, 3000, weigh)
+        assert need > 0
+        cache.weights.zero_()
+        want, lse = vq.kv4_attend(q, cache, t, ints(lens), max_len=3000, add_weights=weigh, return_lse=True)
+        w = cache.weights.clone()
+        cache.weights.zero_()
+        ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+        got, l2 = vq.kv4_attend(q, cache, t, ints(lens), max_len=3000, add_weights=weigh, workspace=ws, return_lse=True)
+        assert torch.equal(got, want) and torch.equal(l2, lse) and torch.equal(cache.weights, w)
+        with pytest.raises(vq.VQError) as e:
+            vq.kv4_attend(q, cache, t, ints(lens), max_len=3000, add_weights=weigh, workspace=ws[:need - 16])
+        assert e.value.status == -8
 
 
 def test_attend_graph_replays(vq):
