@@ -109,7 +109,8 @@ int check_rows(const KvView &v, int32_t total, const int32_t *cu) {
 int check_attend_sizes(const KvView &v, int n_q_heads, int max_len) {
   if (n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % v.hkv != 0 || max_len < 0) return VQ_ERR_SHAPE;
   const int64_t group = n_q_heads / v.hkv;
-  if ((int64_t)v.nseq * v.hkv * ((group + 15) / 16) > ((int64_t)1 << 22)) return VQ_ERR_SHAPE;
+  const int64_t rows = v.hkv * ((group + 15) / 16);
+  if (v.nseq * rows > ((int64_t)1 << 22) || ((int64_t)max_len / 32 + 1) * rows > kMaxInt) return VQ_ERR_SHAPE;
   return VQ_OK;
 }
 

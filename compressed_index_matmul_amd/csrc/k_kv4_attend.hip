@@ -3,9 +3,16 @@
 // For every sequence and key/value head the cache is read once, for up to 16
 // query heads of the group at a time (they are the columns of the matrix
 // products).  A wave walks tiles of 32 slots on its own, with the next tile's
-// loads in flight; the four waves of a workgroup and the splits of a long
-// sequence each keep a running maximum and sum and meet at the end, in LDS
-// and in a second launch, in a fixed order.
+// loads in flight, keeps a running maximum and sum, and meets the other waves
+// of its workgroup in LDS.
+//
+// The tiles of all sequences and heads form one line, which a fixed number of
+// workgroups (what the CUs hold at once) cuts into equal shares: lengths as
+// unequal as may be end together, and one long sequence spreads over the whole
+// chip.  A share covers the end of one row (sequence and head), whole rows, and
+// the beginning of another; the parts of cut rows meet in a second launch, in
+// the order of the line.  Every workgroup finds its place by a prefix sum over
+// the lengths, 64 a step, so the host needs no lengths.
 //
 // Scores: S^T = K Q^T on 16x16x32 fp16 MFMA, a group of 32 channels a
 // product.  Codes are integers, exact in fp16, so a product is exact up to its
@@ -30,8 +37,11 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kLoneWaves = 8;  // of a workgroup that takes a whole sequence and head
 constexpr int kTile = 32;  // slots a wave takes at a time
-constexpr int kPieces = 3072;
 constexpr int kLoneSlots = 1024;
+// Workgroups of four waves that 256 CUs hold at once, by their registers.
+template <int D>
+constexpr int kShares = D == 64 ? 1024 : D == 128 ? 768 : 512;
+int shares_of(int d) { return d == 64 ? kShares<64> : d == 128 ? kShares<128> : kShares<256>; }
 constexpr float kSlack = 8.0f;  // the reference maximum lags by up to 2^8: p <= 256 is in fp16's range
 
 // dword N of the 16 lanes of a row, in all of them.
@@ -138,12 +148,79 @@ struct AttendArgs {
   int hq;
   void *out;
   float *lse;
-  float *part;   // [seq][head][split][D]
-  float *stat;   // [seq][head][split][2]: maximum (log2 domain), sum
-  float *score;  // [seq][head][pitch], log2 domain
+  float *part;    // [share][2][16][D]: a share's part of the row it begins in, and of the one it ends in
+  float *stat;    // [share][2][16][2]: maximum (log2 domain), sum
+  float *whole;   // [seq][head][2]: the same of rows that one share covers (add_weights)
+  float *score;   // [seq][head][pitch], log2 domain (add_weights)
 };
 
-template <int D, bool F16, bool WEIGH, int NW>
+__device__ __forceinline__ int tiles_of(const KvView &c, const AttendPlan &p, int b) {
+  return (min(max(c.lens[b], 0), p.len_cap) + kTile - 1) / kTile;
+}
+
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
+         (int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32;
+}
+
+// The line of tiles: sequence by sequence, in it head by head (`rows` of them).
+struct Line {
+  int64_t total, share;
+  int rows;
+};
+__device__ __forceinline__ uint32_t prefix64(uint32_t v) {  // inclusive, over the wave
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t u = __shfl_up(v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+template <int D>
+__device__ __forceinline__ Line line_of(const KvView &c, const AttendPlan &p) {
+  const int lane = threadIdx.x & 63;
+  int64_t sum = 0;
+  for (int b0 = 0; b0 < c.nseq; b0 += 64) {
+    const uint32_t n = b0 + lane < c.nseq ? tiles_of(c, p, b0 + lane) : 0;  // 64 of below 2^26: within 32 bits
+    sum += (uint32_t)__builtin_amdgcn_readlane((int)prefix64(n), 63);
+  }
+  Line l;
+  l.rows = c.hkv * p.htiles;
+  l.total = sum * l.rows;
+  const int64_t even = (l.total + kShares<D> - 1) / kShares<D>;
+  l.share = max((even + kWaves - 1) / kWaves * kWaves, (int64_t)kWaves);
+  return l;
+}
+// The sequence that holds position pos < total, and where it begins.
+__device__ __forceinline__ int line_find(const KvView &c, const AttendPlan &p, const Line &l, int64_t pos, int64_t *begin) {
+  const int lane = threadIdx.x & 63;
+  int64_t base = 0;
+  for (int b0 = 0;; b0 += 64) {
+    const uint32_t n = b0 + lane < c.nseq ? tiles_of(c, p, b0 + lane) : 0;
+    const uint32_t upto = prefix64(n);
+    const uint64_t past = __ballot(base + (int64_t)upto * l.rows > pos);
+    if (past || b0 + 64 >= c.nseq) {
+      const int at = past ? __builtin_ctzll(past) : 63;
+      *begin = base + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)(upto - n), at) * l.rows;
+      return min(b0 + at, c.nseq - 1);
+    }
+    base += (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)upto, 63) * l.rows;
+  }
+}
+// Where sequence b begins.
+__device__ __forceinline__ int64_t line_begin(const KvView &c, const AttendPlan &p, const Line &l, int b) {
+  const int lane = threadIdx.x & 63;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < b; b0 += 64) {
+    const uint32_t n = b0 + lane < b ? tiles_of(c, p, b0 + lane) : 0;
+    base += (uint32_t)__builtin_amdgcn_readlane((int)prefix64(n), 63);
+  }
+  return base * l.rows;
+}
+
+// LONE: a workgroup of NW waves a row, all of it.
+template <int D, bool F16, bool WEIGH, int NW, bool LONE>
 __global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPlan p, AttendArgs a) {
   constexpr int kThreads = NW * kWave, kWaves = NW;
   constexpr int DG = D / 32, CH = D / 16;
@@ -151,22 +228,43 @@ __global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPla
   __shared__ float s_o[kWaves][16][kPitch];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
 
-  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int id = blockIdx.x;
-  const int split = id % p.splits;
-  id /= p.splits;
-  const int kvh = id % c.hkv;
-  id /= c.hkv;
-  const int ht = id % p.htiles;
-  const int b = id / p.htiles;
-
+  Line line{};
+  int64_t pos = 0, pos_end = 1;
+  if (!LONE) {
+    line = line_of<D>(c, p);
+    line.total = uniform(line.total);
+    line.share = uniform(line.share);
+    pos = blockIdx.x * line.share;
+    pos_end = min(pos + line.share, line.total);
+  }
+  const int64_t pos0 = pos;
+  while (pos < pos_end) {
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));  // anew for each row: what follows from it would else be kept in registers throughout
+  const int lane = tid & 63, col = lane & 15, h4 = lane >> 4;
+  int b, row, t_begin, t_end, ntiles;
+  if (LONE) {
+    row = blockIdx.x % (c.hkv * p.htiles);
+    b = blockIdx.x / (c.hkv * p.htiles);
+    ntiles = tiles_of(c, p, b);
+    t_begin = 0;
+    t_end = ntiles;
+    pos = pos_end;
+  } else {
+    int64_t begin;
+    b = __builtin_amdgcn_readfirstlane(line_find(c, p, line, pos, &begin));
+    ntiles = __builtin_amdgcn_readfirstlane(tiles_of(c, p, b));
+    const int in = (int)(pos - begin);  // a sequence's tiles over all rows are below 2^31
+    row = __builtin_amdgcn_readfirstlane(in / ntiles);
+    t_begin = __builtin_amdgcn_readfirstlane(in - row * ntiles);
+    t_end = __builtin_amdgcn_readfirstlane((int)min((int64_t)ntiles, t_begin + (pos_end - pos)));
+    pos += t_end - t_begin;
+  }
+  const int kvh = row / p.htiles, ht = row - kvh * p.htiles;
   const int len = min(max(c.lens[b], 0), p.len_cap);
-  const int ntiles = (len + kTile - 1) / kTile;
-  const int t_begin = min(split * p.tiles, ntiles), t_end = min(t_begin + p.tiles, ntiles);
-  const int heads = min(16, p.group - ht * 16);   // of this workgroup
+  const int heads = min(16, p.group - ht * 16);   // of this row
   const int head0 = kvh * p.group + ht * 16;
-  const int col = lane & 15, h4 = lane >> 4;
 
   // the queries, in fp16 after a power-of-two rescale per head, in the order of the unpacked codes
   half8_t qf[DG];
@@ -302,7 +400,9 @@ __global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPla
     }
   }
 
-  // the four waves meet
+  // the waves meet
+  const bool whole = LONE || (t_begin == 0 && t_end == ntiles);
+  const int side = pos - (t_end - t_begin) == pos0 && t_begin > 0 ? 0 : 1;  // 0: the row began in an earlier share
   lsum = sum_xor32(sum_xor16(lsum));
   if (col < heads) {
     if (h4 == 0) s_m[wave][col] = mref, s_l[wave][col] = lsum;
@@ -314,7 +414,7 @@ __global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPla
             float4_t{acc[x][i], acc[x + 1][i], acc[x + 2][i], acc[x + 3][i]};
   }
   __syncthreads();
-  for (int e = threadIdx.x * 4; e < heads * D; e += kThreads * 4) {
+  for (int e = tid * 4; e < heads * D; e += kThreads * 4) {
     const int h = e / D, d = e % D;
     float top = -INFINITY;
 #pragma unroll
@@ -330,32 +430,63 @@ __global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPla
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(ow[i], f, o[i]);
     }
-    const int64_t row = (int64_t)b * a.hq + head0 + h;
-    if (p.splits == 1) {
+    const int64_t at = (int64_t)b * a.hq + head0 + h;
+    if (whole) {
       const float r = l == 0.0f ? 0.0f : 1.0f / l;
       const uint2_t w = {pack16<F16>(o[0] * r, o[1] * r), pack16<F16>(o[2] * r, o[3] * r)};
-      *reinterpret_cast<uint2_t *>(static_cast<uint16_t *>(a.out) + row * D + d) = w;
-      if (d == 0 && a.lse) a.lse[row] = (__builtin_amdgcn_logf(l) + m0) * kLn2;
+      *reinterpret_cast<uint2_t *>(static_cast<uint16_t *>(a.out) + at * D + d) = w;
+      if (d == 0) {
+        if (a.lse) a.lse[at] = (__builtin_amdgcn_logf(l) + m0) * kLn2;
+        if (WEIGH) a.whole[at * 2] = top, a.whole[at * 2 + 1] = l;
+      }
     } else {
-      *reinterpret_cast<float4_t *>(a.part + (row * p.splits + split) * D + d) = o;
+      const int64_t piece = ((int64_t)blockIdx.x * 2 + side) * 16 + h;
+      *reinterpret_cast<float4_t *>(a.part + piece * D + d) = o;
+      if (d == 0) a.stat[piece * 2] = top, a.stat[piece * 2 + 1] = l;
     }
-    if (d == 0 && (WEIGH || p.splits > 1)) {
-      a.stat[(row * p.splits + split) * 2] = top;
-      a.stat[(row * p.splits + split) * 2 + 1] = l;
-    }
+  }
+  __syncthreads();  // the LDS is free for the next row
   }
 }
 
-// Maximum and sum of one head over its splits, by one wave.
-__device__ __forceinline__ void head_stats(const float *stat, int splits, float *top, float *sum) {
+// The parts of one row: the shares from `first` to `last` of the line, each at
+// side 1 of the first and side 0 of the others.
+struct Parts {
+  int first, n;
+  bool whole, empty;
+};
+template <int D>
+__device__ __forceinline__ Parts parts_of(const KvView &c, const AttendPlan &p, const Line &l, int b, int row) {
+  const int nt = tiles_of(c, p, b);
+  const int64_t begin = line_begin(c, p, l, b) + (int64_t)row * nt, end = begin + nt;
+  Parts r;
+  r.empty = nt == 0;
+  r.first = (int)(begin / l.share);
+  r.n = nt == 0 ? 0 : (int)((end - 1) / l.share) - r.first + 1;
+  r.whole = r.n == 1;
+  return r;
+}
+__device__ __forceinline__ int64_t part_at(const Parts &r, int i, int h) {
+  return ((int64_t)(r.first + i) * 2 + (i == 0 ? 1 : 0)) * 16 + h;
+}
+// Maximum and sum of one head over its parts, by one wave.
+__device__ __forceinline__ void head_stats(const AttendArgs &a, const Parts &r, int64_t at, int h, float *top, float *sum) {
   const int lane = threadIdx.x & 63;
+  if (r.whole) {
+    *top = a.whole[at * 2] == -INFINITY ? 0.0f : a.whole[at * 2];
+    *sum = a.whole[at * 2 + 1];
+    return;
+  }
   float m = -INFINITY;
-  for (int s = lane; s < splits; s += kWave) m = fmaxf(m, stat[2 * s]);
+  for (int i = lane; i < r.n; i += kWave) m = fmaxf(m, a.stat[part_at(r, i, h) * 2]);
 #pragma unroll
   for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
   const float m0 = m == -INFINITY ? 0.0f : m;
   float l = 0.0f;
-  for (int s = lane; s < splits; s += kWave) l = __builtin_fmaf(stat[2 * s + 1], __builtin_amdgcn_exp2f(stat[2 * s] - m0), l);
+  for (int i = lane; i < r.n; i += kWave) {
+    const float *st = a.stat + part_at(r, i, h) * 2;
+    l = __builtin_fmaf(st[1], __builtin_amdgcn_exp2f(st[0] - m0), l);
+  }
 #pragma unroll
   for (int o = 32; o; o >>= 1) l += __shfl_xor(l, o);
   *top = m0;
@@ -364,25 +495,31 @@ __device__ __forceinline__ void head_stats(const float *stat, int splits, float 
 
 constexpr int kWeighSlots = kThreads * 4;  // slots of a workgroup of the weights' part
 
-// The splits meet: the first `out_blocks` workgroups take a head's output
-// each (none when there is one split), the others the weights of a run of
-// slots of one sequence and key/value head.
+// The first `out_blocks` workgroups take a head's output each, where its row
+// was cut (or is empty); the others the weights of a run of slots of one
+// sequence and key/value head.
 template <int D, bool F16>
 __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, AttendArgs a, int out_blocks, int chunks) {
+  const Line line = line_of<D>(c, p);
   if ((int)blockIdx.x < out_blocks) {
-    constexpr int kSub = kThreads / (D / 4);  // splits summed side by side, four channels a thread
+    constexpr int kSub = kThreads / (D / 4);  // parts summed side by side, four channels a thread
     __shared__ float s_part[kSub][D];
-    const int64_t row = blockIdx.x;
-    const float *stat = a.stat + row * p.splits * 2;
+    const int64_t at = blockIdx.x;
+    const int b = (int)(at / a.hq), head = (int)(at - (int64_t)b * a.hq);
+    const int kvh = head / p.group, ht = (head - kvh * p.group) / 16, h = (head - kvh * p.group) % 16;
+    const Parts parts = parts_of<D>(c, p, line, b, kvh * p.htiles + ht);
+    if (parts.whole) return;
     float top, sum;
-    head_stats(stat, p.splits, &top, &sum);
+    head_stats(a, parts, at, h, &top, &sum);
     const int d = threadIdx.x % (D / 4) * 4, sub = threadIdx.x / (D / 4);
     float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = sub; s < p.splits; s += kSub) {
-      const float f = __builtin_amdgcn_exp2f(stat[2 * s] - top);
-      const float4_t v = *reinterpret_cast<const float4_t *>(a.part + (row * p.splits + s) * D + d);
+#pragma unroll 4
+    for (int i = sub; i < parts.n; i += kSub) {
+      const int64_t piece = part_at(parts, i, h);
+      const float f = __builtin_amdgcn_exp2f(a.stat[piece * 2] - top);
+      const float4_t v = *reinterpret_cast<const float4_t *>(a.part + piece * D + d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], f, o[i]);
+      for (int j = 0; j < 4; ++j) o[j] = __builtin_fmaf(v[j], f, o[j]);
     }
     *reinterpret_cast<float4_t *>(&s_part[sub][d]) = o;
     __syncthreads();
@@ -390,13 +527,13 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
     for (int x = threadIdx.x * 2; x < D; x += kThreads * 2) {
       float y0 = 0.0f, y1 = 0.0f;
 #pragma unroll
-      for (int s = 0; s < kSub; ++s) y0 += s_part[s][x], y1 += s_part[s][x + 1];
-      *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + row * D + x) = pack16<F16>(y0 * r, y1 * r);
+      for (int i = 0; i < kSub; ++i) y0 += s_part[i][x], y1 += s_part[i][x + 1];
+      *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at * D + x) = pack16<F16>(y0 * r, y1 * r);
     }
-    if (threadIdx.x == 0 && a.lse) a.lse[row] = (__builtin_amdgcn_logf(sum) + top) * kLn2;
+    if (threadIdx.x == 0 && a.lse) a.lse[at] = (__builtin_amdgcn_logf(sum) + top) * kLn2;
     return;
   }
-  __shared__ float s_top[kWave], s_inv[kWave];
+  __shared__ float s_top[16], s_inv[16];
   int id = blockIdx.x - out_blocks;
   const int chunk = id % chunks;
   id /= chunks;
@@ -406,20 +543,21 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
   const int slot = chunk * kWeighSlots + threadIdx.x * 4;
   float4_t w = {0.0f, 0.0f, 0.0f, 0.0f};
   const int wave = threadIdx.x >> 6;
-  for (int g0 = 0; g0 < p.group; g0 += kWave) {  // heads of the group, 64 at a time
-    const int ng = min(kWave, p.group - g0);
-    const int64_t row0 = (int64_t)b * a.hq + kvh * p.group + g0;
+  for (int ht = 0; ht < p.htiles; ++ht) {  // heads of the group, 16 at a time
+    const int ng = min(16, p.group - ht * 16);
+    const int64_t at0 = (int64_t)b * a.hq + kvh * p.group + ht * 16;
+    const Parts parts = parts_of<D>(c, p, line, b, kvh * p.htiles + ht);
     __syncthreads();
     for (int g = wave; g < ng; g += kWaves) {
       float top, sum;
-      head_stats(a.stat + (row0 + g) * p.splits * 2, p.splits, &top, &sum);
+      head_stats(a, parts, at0 + g, g, &top, &sum);
       if ((threadIdx.x & 63) == 0) s_top[g] = top, s_inv[g] = sum == 0.0f ? 0.0f : 1.0f / sum;
     }
     __syncthreads();
     if (slot < len)
 #pragma unroll 8
       for (int g = 0; g < ng; ++g) {
-        const float4_t x = *reinterpret_cast<const float4_t *>(a.score + (row0 + g) * p.score_pitch + slot);
+        const float4_t x = *reinterpret_cast<const float4_t *>(a.score + (at0 + g) * p.score_pitch + slot);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(x[i] - s_top[g]), s_inv[g], w[i]);
       }
@@ -439,45 +577,40 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
 
 template <int D, bool F16>
 hipError_t attend_d(const KvView &c, const AttendPlan &p, const AttendArgs &a, bool weigh, hipStream_t s) {
-  const unsigned blocks = (unsigned)((int64_t)c.nseq * c.hkv * p.htiles * p.splits);
-  if (weigh) k_kv4_attend<D, F16, true, kWaves><<<blocks, kThreads, 0, s>>>(c, p, a);
-  else if (p.lone) k_kv4_attend<D, F16, false, kLoneWaves><<<blocks, kLoneWaves * kWave, 0, s>>>(c, p, a);
-  else k_kv4_attend<D, F16, false, kWaves><<<blocks, kThreads, 0, s>>>(c, p, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || (p.splits == 1 && !weigh)) return e;
-  const int out_blocks = p.splits > 1 ? c.nseq * a.hq : 0;
+  if (p.lone) {
+    k_kv4_attend<D, F16, false, kLoneWaves, true><<<c.nseq * c.hkv * p.htiles, kLoneWaves * kWave, 0, s>>>(c, p, a);
+    return hipGetLastError();
+  }
   const int chunks = weigh ? (p.len_cap + kWeighSlots - 1) / kWeighSlots : 0;
-  const int64_t grid = out_blocks + (int64_t)chunks * c.nseq * c.hkv;
-  if (grid == 0) return hipSuccess;
+  const int64_t grid = (int64_t)c.nseq * a.hq + (int64_t)chunks * c.nseq * c.hkv;
   if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
-  k_kv4_join<D, F16><<<(unsigned)grid, kThreads, 0, s>>>(c, p, a, out_blocks, chunks);
+  if (weigh) k_kv4_attend<D, F16, true, kWaves, false><<<kShares<D>, kThreads, 0, s>>>(c, p, a);
+  else k_kv4_attend<D, F16, false, kWaves, false><<<kShares<D>, kThreads, 0, s>>>(c, p, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_kv4_join<D, F16><<<(unsigned)grid, kThreads, 0, s>>>(c, p, a, c.nseq * a.hq, chunks);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// One workgroup a row where rows are short and fewer than the CUs: no second
+// launch.
 AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add_weights) {
   AttendPlan p{};
   p.group = n_q_heads / c.hkv;
   p.htiles = (p.group + 15) / 16;
   p.len_cap = (int)std::min<int64_t>(max_len, (int64_t)c.mp * c.ps);
-  // Pieces of equal size, so that sequences of unequal length spread evenly: about 3072 of them (twelve
-  // workgroups a CU) if every sequence were as long as the bound, but not below the 128 slots that the waves
-  // take in one round.
-  const int64_t work = (int64_t)c.nseq * c.hkv * p.htiles;
-  const int64_t round_slots = kWaves * kTile;
-  const int64_t rounds = std::max<int64_t>(1, ((int64_t)p.len_cap * work + kPieces * round_slots - 1) / (kPieces * round_slots));
-  p.tiles = (int)std::min<int64_t>(rounds * kWaves, ((int64_t)1 << 26));
-  p.splits = (int)std::max<int64_t>(1, ((int64_t)p.len_cap + p.tiles * kTile - 1) / ((int64_t)p.tiles * kTile));
-  p.lone = !add_weights && p.splits > 1 && p.len_cap <= kLoneSlots && work <= 256;
-  if (p.lone) p.splits = 1, p.tiles = (p.len_cap + kTile - 1) / kTile;
+  const int64_t rows = (int64_t)c.nseq * c.hkv * p.htiles;
+  p.lone = !add_weights && p.len_cap <= kLoneSlots && rows <= 256;
+  if (p.lone) return p;
   p.score_pitch = (p.len_cap + kTile - 1) / kTile * kTile;
-  const size_t rows = (size_t)c.nseq * n_q_heads;
   auto round = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  p.part_off = 0;
-  p.stat_off = p.splits > 1 ? round(rows * p.splits * c.d * 4) : 0;
-  p.score_off = p.stat_off + (p.splits > 1 || add_weights ? round(rows * p.splits * 8) : 0);
-  p.bytes = p.score_off + (add_weights ? round(rows * p.score_pitch * 4) : 0);
+  const size_t pieces = (size_t)shares_of(c.d) * 2 * 16, heads = (size_t)c.nseq * n_q_heads;
+  p.stat_off = round(pieces * c.d * 4);
+  p.whole_off = p.stat_off + round(pieces * 8);
+  p.score_off = p.whole_off + (add_weights ? round(heads * 8) : 0);
+  p.bytes = p.score_off + (add_weights ? round(heads * p.score_pitch * 4) : 0);
   return p;
 }
 
@@ -485,8 +618,9 @@ hipError_t launch_kv4_attend(const KvView &c, const AttendPlan &p, const void *q
                              int n_q_heads, float scale, bool add_weights, void *out, float *lse, void *ws,
                              hipStream_t s) {
   char *w = static_cast<char *>(ws);
-  AttendArgs a{q, q_ts, q_hs, scale, n_q_heads, out, lse, reinterpret_cast<float *>(w + p.part_off),
-               reinterpret_cast<float *>(w + p.stat_off), reinterpret_cast<float *>(w + p.score_off)};
+  AttendArgs a{q,   q_ts, q_hs, scale, n_q_heads, out, lse, reinterpret_cast<float *>(w),
+               reinterpret_cast<float *>(w + p.stat_off), reinterpret_cast<float *>(w + p.whole_off),
+               reinterpret_cast<float *>(w + p.score_off)};
   if (c.d == 64) return f16 ? attend_d<64, true>(c, p, a, add_weights, s) : attend_d<64, false>(c, p, a, add_weights, s);
   if (c.d == 128)
     return f16 ? attend_d<128, true>(c, p, a, add_weights, s) : attend_d<128, false>(c, p, a, add_weights, s);

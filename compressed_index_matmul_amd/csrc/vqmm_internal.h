@@ -133,12 +133,10 @@ hipError_t launch_kv4_read(const KvView &c, const int32_t *cu, int total, int dt
 struct AttendPlan {
   int group;        // query heads per key/value head
   int htiles;       // 16-head tiles of a group
-  int tiles;        // 32-slot tiles of one piece of a sequence and head
-  int splits;       // pieces that the longest sequence may have
-  bool lone;        // short: one workgroup of more waves takes it whole
+  bool lone;        // short and few rows: one workgroup of more waves takes each whole
   int len_cap;      // lengths are clamped to this
   int score_pitch;  // floats per head of stored scores (add_weights)
-  size_t part_off, stat_off, score_off, bytes;
+  size_t stat_off, whole_off, score_off, bytes;
 };
 AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add_weights);
 hipError_t launch_kv4_attend(const KvView &c, const AttendPlan &p, const void *q, int64_t q_ts, int64_t q_hs, bool f16,
