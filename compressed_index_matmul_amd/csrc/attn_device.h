@@ -29,6 +29,10 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
 }
 
+// Smallest / largest, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) { return __builtin_elementwise_minimum(a, b); }
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Largest value of the lanes l, l ^ 32.
 __device__ __forceinline__ float max_xor32(float v) {
   const uint32_t u = __float_as_uint(v);

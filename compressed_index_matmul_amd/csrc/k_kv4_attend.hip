@@ -39,27 +39,38 @@ constexpr int kLoneWaves = 8;  // of a workgroup that takes a whole sequence and
 constexpr int kTile = 32;  // slots a wave takes at a time
 constexpr int kLoneSlots = 1024;
 // Workgroups of four waves that 256 CUs hold at once, by their registers.
-template <int D>
-constexpr int kShares = D == 64 ? 1024 : D == 128 ? 768 : 512;
-int shares_of(int d) { return d == 64 ? kShares<64> : d == 128 ? kShares<128> : kShares<256>; }
+// Heads of 128: four workgroups a CU (128 registers, 8 bytes spilled) took 41 us where three took 45 for 32 x 4096
+// slots of 32/8 heads; with weights, whose scores are written as well, four took 143 us and three 138 for the 300,000
+// slots of 64/8 heads.
+template <int D, bool WEIGH>
+constexpr int kSharesPerCu = D == 64 ? 4 : D == 128 ? (WEIGH ? 3 : 4) : 2;
+template <int D, bool WEIGH>
+constexpr int kShares = 256 * kSharesPerCu<D, WEIGH>;
+int shares_of(int d) { return d == 64 ? kShares<64, false> : d == 128 ? kShares<128, false> : kShares<256, false>; }  // the most
 constexpr float kSlack = 8.0f;  // the reference maximum lags by up to 2^8: p <= 256 is in fp16's range
 
 // dword N of the 16 lanes of a row, in all of them.
 template <int N>
 __device__ __forceinline__ uint32_t row_bcast(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + N, 0xF, 0xF, false);
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x150 + N, 0xF, 0xF, true);
 }
 
+// Masks and bias of the unpacking, in registers: an instruction that takes
+// all three operands holds no literals.
+struct Unpack {
+  uint32_t lo = 0x000f000fu, hi = 0x00f000f0u, bias = 0x64006400u;
+  __device__ __forceinline__ Unpack() { asm("" : "+v"(lo), "+v"(hi), "+v"(bias)); }
+};
 // Eight 4-bit codes of a word as fp16 integers, in the order of the bits 0,
 // 16, 4, 20, 8, 24, 12, 28.  1024 + n has the bits 0x6400 | n in fp16, 1024 +
 // 16 n the bits 0x6400 | n << 4; one packed operation takes the 1024 off.
-__device__ __forceinline__ half2_t code_lo(uint32_t w) {
+__device__ __forceinline__ half2_t code_lo(const Unpack &k, uint32_t w) {
   const half2_t bias = {(_Float16)1024.0f, (_Float16)1024.0f};
-  return as_h2((w & 0x000f000fu) | 0x64006400u) - bias;
+  return as_h2((w & k.lo) | k.bias) - bias;
 }
-__device__ __forceinline__ half2_t code_hi(uint32_t w) {
+__device__ __forceinline__ half2_t code_hi(const Unpack &k, uint32_t w) {
   const half2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f}, bias = {(_Float16)64.0f, (_Float16)64.0f};
-  return as_h2((w & 0x00f000f0u) | 0x64006400u) * sixteenth - bias;
+  return as_h2((w & k.hi) | k.bias) * sixteenth - bias;
 }
 __device__ __forceinline__ half8_t join(half2_t a, half2_t b, half2_t c, half2_t d) {
   return half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
@@ -92,31 +103,38 @@ struct Tile {
   Words<DG> v[2];        // two quads of slots: a lane's D / 16 channels
   uint4_t vs[2];
 
-  __device__ __forceinline__ void load(const uint8_t *kb, const uint8_t *vb, const uint16_t *ksb, const uint16_t *vsb,
-                                       int t, int lane) {
-    const int c = lane & 15, h4 = lane >> 4;
+  // From the tile's first byte of keys or values and of their steps, the same
+  // for every lane; the lane's offsets stay the same from tile to tile.
+  __device__ __forceinline__ void load_keys(const uint8_t *kb, const uint8_t *sb, int lane) {
+    const uint32_t c = lane & 15, h4 = lane >> 4;
+    const uint32_t ko = c * (D / 2) + h4 * (DG * 4), so = h4 * (DG * 16) + (SW == 1 ? (c & (4 * DG - 1)) * 4 : c * 8);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      k[u].load(kb + (t * kTile + 16 * u + c) * (D / 2) + h4 * (DG * 4));
-      const uint32_t *sp = reinterpret_cast<const uint32_t *>(ksb + (t * (kTile / 4) + 4 * u + h4) * (DG * 8));
-      if (SW == 1) ks[u][0] = sp[c & (4 * DG - 1)];
+      k[u].load(kb + u * (8 * D) + ko);
+      if (SW == 1) ks[u][0] = *reinterpret_cast<const uint32_t *>(sb + u * (DG * 64) + so);
       else {
-        const uint2_t x = reinterpret_cast<const uint2_t *>(sp)[c];
+        const uint2_t x = *reinterpret_cast<const uint2_t *>(sb + u * (DG * 64) + so);
         ks[u][0] = x[0], ks[u][SW - 1] = x[1];
       }
-      const int quad = t * (kTile / 4) + 4 * u + h4;
-      v[u].load(vb + quad * (2 * D) + c * (D / 8));
-      vs[u] = *reinterpret_cast<const uint4_t *>(vsb + quad * (DG * 8) + (c * DG / 16) * 8);
+    }
+  }
+  __device__ __forceinline__ void load_values(const uint8_t *vb, const uint8_t *sb, int lane) {
+    const uint32_t c = lane & 15, h4 = lane >> 4;
+    const uint32_t vo = h4 * (2 * D) + c * (D / 8), so = h4 * (DG * 16) + (c * DG / 16) * 16;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      v[u].load(vb + u * (8 * D) + vo);
+      vs[u] = *reinterpret_cast<const uint4_t *>(sb + u * (DG * 64) + so);
     }
   }
 };
 
 // One group of the scores of a half: S[i] += s_i D[i] + m_i qsum.
 template <int D, int J>
-__device__ __forceinline__ void add_group(float *S, const Tile<D> &t, int u, half8_t qf, float qsum) {
+__device__ __forceinline__ void add_group(float *S, const Tile<D> &t, int u, half8_t qf, float qsum, const Unpack &k) {
   constexpr int SW = Tile<D>::SW;
   const uint32_t w = t.k[u].w[J];
-  const half8_t kf = join(code_lo(w), code_hi(w), code_lo(w >> 8), code_hi(w >> 8));
+  const half8_t kf = join(code_lo(k, w), code_hi(k, w), code_lo(k, w >> 8), code_hi(k, w >> 8));
   const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
   const float4_t dot = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf, zero, 0, 0, 0);
   const half2_t s01 = as_h2(row_bcast<(4 * J + 0) / SW>(t.ks[u][0]));
@@ -131,14 +149,15 @@ __device__ __forceinline__ void add_group(float *S, const Tile<D> &t, int u, hal
 
 template <int D, int J>
 struct AddGroups {
-  static __device__ __forceinline__ void run(float *S, const Tile<D> &t, int u, const half8_t *qf, const float *qsum) {
-    AddGroups<D, J - 1>::run(S, t, u, qf, qsum);
-    add_group<D, J>(S, t, u, qf[J], qsum[J]);
+  static __device__ __forceinline__ void run(float *S, const Tile<D> &t, int u, const half8_t *qf, const float *qsum,
+                                             const Unpack &k) {
+    AddGroups<D, J - 1>::run(S, t, u, qf, qsum, k);
+    add_group<D, J>(S, t, u, qf[J], qsum[J], k);
   }
 };
 template <int D>
 struct AddGroups<D, -1> {
-  static __device__ __forceinline__ void run(float *, const Tile<D> &, int, const half8_t *, const float *) {}
+  static __device__ __forceinline__ void run(float *, const Tile<D> &, int, const half8_t *, const float *, const Unpack &) {}
 };
 
 struct AttendArgs {
@@ -177,7 +196,7 @@ __device__ __forceinline__ uint32_t prefix64(uint32_t v) {  // inclusive, over t
   }
   return v;
 }
-template <int D>
+template <int D, bool WEIGH>
 __device__ __forceinline__ Line line_of(const KvView &c, const AttendPlan &p) {
   const int lane = threadIdx.x & 63;
   int64_t sum = 0;
@@ -188,7 +207,7 @@ __device__ __forceinline__ Line line_of(const KvView &c, const AttendPlan &p) {
   Line l;
   l.rows = c.hkv * p.htiles;
   l.total = sum * l.rows;
-  const int64_t even = (l.total + kShares<D> - 1) / kShares<D>;
+  const int64_t even = (l.total + kShares<D, WEIGH> - 1) / kShares<D, WEIGH>;
   l.share = max((even + kWaves - 1) / kWaves * kWaves, (int64_t)kWaves);
   return l;
 }
@@ -221,7 +240,7 @@ __device__ __forceinline__ int64_t line_begin(const KvView &c, const AttendPlan 
 
 // LONE: a workgroup of NW waves a row, all of it.
 template <int D, bool F16, bool WEIGH, int NW, bool LONE>
-__global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPlan p, AttendArgs a) {
+__global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) void k_kv4_attend(KvView c, AttendPlan p, AttendArgs a) {
   constexpr int kThreads = NW * kWave, kWaves = NW;
   constexpr int DG = D / 32, CH = D / 16;
   constexpr int kPitch = D + 4;  // floats of a head's row in LDS: 16-byte pieces of 16 rows fall on different banks
@@ -232,7 +251,7 @@ __global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPla
   Line line{};
   int64_t pos = 0, pos_end = 1;
   if (!LONE) {
-    line = line_of<D>(c, p);
+    line = line_of<D, WEIGH>(c, p);
     line.total = uniform(line.total);
     line.share = uniform(line.share);
     pos = blockIdx.x * line.share;
@@ -318,31 +337,40 @@ __global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPla
 
   const int tpp = c.ps / kTile;  // tiles of a page
   const int64_t code_head = (int64_t)c.ps * (D / 2), scale_head = (int64_t)c.ps * (DG * 2);
-  auto fetch = [&](Tile<D> &t, int tile) {
+  // Keys and values of the next tile go into the registers of this one as soon
+  // as those are used up: half a round before they are wanted.
+  Tile<D> cur;
+  const uint8_t *next_v, *next_vs;
+  auto fetch_keys = [&](int tile) {
     const int pi = tile / tpp;
     const int64_t page = page_of(c, b, pi);
-    const uint8_t *kb = c.codes + (page * 2 * c.hkv + kvh) * code_head;
-    const uint16_t *sb = c.scales + (page * 2 * c.hkv + kvh) * scale_head;
-    t.load(kb, kb + c.hkv * code_head, sb, sb + c.hkv * scale_head, tile - pi * tpp, lane);
+    const int at = tile - pi * tpp;
+    const uint8_t *kb = c.codes + (page * 2 * c.hkv + kvh) * code_head + at * (kTile * D / 2);
+    const uint8_t *sb = reinterpret_cast<const uint8_t *>(c.scales + (page * 2 * c.hkv + kvh) * scale_head) + at * (kTile * DG * 4);
+    cur.load_keys(kb, sb, lane);
+    next_v = kb + c.hkv * code_head;
+    next_vs = sb + 2 * c.hkv * scale_head;
   };
-
-  Tile<D> cur, next;
+  const Unpack unpack;
   int tile = t_begin + wave;
-  if (tile < t_end) fetch(next, tile);
+  if (tile < t_end) {
+    fetch_keys(tile);
+    cur.load_values(next_v, next_vs, lane);
+  }
   for (; tile < t_end; tile += kWaves) {
-    cur = next;
-    if (tile + kWaves < t_end) fetch(next, tile + kWaves);
-
     float S[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-    for (int u = 0; u < 2; ++u) AddGroups<D, DG - 1>::run(S[u], cur, u, qf, qsum);
+    for (int u = 0; u < 2; ++u) {
+      AddGroups<D, DG - 1>::run(S[u], cur, u, qf, qsum, unpack);
+      // one half's products and broadcast steps in registers at a time, not both until after the loads below
+      asm volatile("" : "+v"(S[u][0]), "+v"(S[u][1]), "+v"(S[u][2]), "+v"(S[u][3]));
+    }
+    const bool more = tile + kWaves < t_end;
+    if (more) fetch_keys(tile + kWaves);
 
     const int left = len - tile * kTile;  // slots of the tile that exist
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) S[u][i] *= cs;
     if (left < kTile) {  // the last tile: slots past the end count for nothing, whatever they hold
+      asm volatile("");  // a branch, not selects in every tile
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int in = left - 16 * u - 4 * h4;  // of the lane's four slots
@@ -354,13 +382,15 @@ __global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPla
     }
     if (WEIGH && col < heads) {
       float *sp = a.score + ((int64_t)b * a.hq + head0 + col) * p.score_pitch + tile * kTile + 4 * h4;
-      *reinterpret_cast<float4_t *>(sp) = float4_t{S[0][0], S[0][1], S[0][2], S[0][3]};
-      *reinterpret_cast<float4_t *>(sp + 16) = float4_t{S[1][0], S[1][1], S[1][2], S[1][3]};
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        *reinterpret_cast<float4_t *>(sp + 16 * u) = float4_t{S[u][0] * cs, S[u][1] * cs, S[u][2] * cs, S[u][3] * cs};
     }
 
-    float top = fmaxf(fmaxf(fmaxf(S[0][0], S[0][1]), fmaxf(S[0][2], S[0][3])),
-                      fmaxf(fmaxf(S[1][0], S[1][1]), fmaxf(S[1][2], S[1][3])));
-    top = max_xor32(max_xor16(top));
+    // (a NaN spoils its own head's sum whatever the maximum is)
+    float top = max_nan(max_nan(max_nan(S[0][0], S[0][1]), max_nan(S[0][2], S[0][3])),
+                        max_nan(max_nan(S[1][0], S[1][1]), max_nan(S[1][2], S[1][3])));
+    top = max_xor32(max_xor16(top)) * cs;
     if (__any(top > mref + kSlack)) {
       const float mnew = fmaxf(mref, top);
       const float f = mnew == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mref - mnew);
@@ -375,7 +405,7 @@ __global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPla
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        P[u][i] = __builtin_amdgcn_exp2f(S[u][i] - m0);
+        P[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[u][i], cs, -m0));
         lsum += P[u][i];
       }
     const uint4_t pw = {pack16<true>(P[0][0], P[0][1]), pack16<true>(P[0][2], P[0][3]),
@@ -391,13 +421,15 @@ __global__ __launch_bounds__(NW *kWave, 2) void k_kv4_attend(KvView c, AttendPla
 #pragma unroll
     for (int i = 0; i < DG; ++i) {  // two pairs of channels a word: 2 i' = CH channels in all
       const uint32_t w0 = cur.v[0].w[i], w1 = cur.v[1].w[i];
-      const half8_t lo = join(code_lo(w0) * sv[0] + mv[0], code_lo(w0 >> 8) * sv[1] + mv[1],
-                              code_lo(w1) * sv[2] + mv[2], code_lo(w1 >> 8) * sv[3] + mv[3]);
-      const half8_t hi = join(code_hi(w0) * sv[0] + mv[0], code_hi(w0 >> 8) * sv[1] + mv[1],
-                              code_hi(w1) * sv[2] + mv[2], code_hi(w1 >> 8) * sv[3] + mv[3]);
+      const Unpack &k = unpack;
+      const half8_t lo = join(code_lo(k, w0) * sv[0] + mv[0], code_lo(k, w0 >> 8) * sv[1] + mv[1],
+                              code_lo(k, w1) * sv[2] + mv[2], code_lo(k, w1 >> 8) * sv[3] + mv[3]);
+      const half8_t hi = join(code_hi(k, w0) * sv[0] + mv[0], code_hi(k, w0 >> 8) * sv[1] + mv[1],
+                              code_hi(k, w1) * sv[2] + mv[2], code_hi(k, w1 >> 8) * sv[3] + mv[3]);
       acc[2 * i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, pf, acc[2 * i], 0, 0, 0);
       acc[2 * i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, pf, acc[2 * i + 1], 0, 0, 0);
     }
+    if (more) cur.load_values(next_v, next_vs, lane);
   }
 
   // the waves meet
@@ -498,9 +530,9 @@ constexpr int kWeighSlots = kThreads * 4;  // slots of a workgroup of the weight
 // The first `out_blocks` workgroups take a head's output each, where its row
 // was cut (or is empty); the others the weights of a run of slots of one
 // sequence and key/value head.
-template <int D, bool F16>
+template <int D, bool F16, bool WEIGH>
 __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, AttendArgs a, int out_blocks, int chunks) {
-  const Line line = line_of<D>(c, p);
+  const Line line = line_of<D, WEIGH>(c, p);
   if ((int)blockIdx.x < out_blocks) {
     constexpr int kSub = kThreads / (D / 4);  // parts summed side by side, four channels a thread
     __shared__ float s_part[kSub][D];
@@ -575,6 +607,12 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
   }
 }
 
+template <int D, bool F16, bool WEIGH>
+hipError_t attend_shares(const KvView &c, const AttendPlan &p, const AttendArgs &a, hipStream_t s) {
+  k_kv4_attend<D, F16, WEIGH, kWaves, false><<<kShares<D, WEIGH>, kThreads, 0, s>>>(c, p, a);
+  return hipGetLastError();
+}
+
 template <int D, bool F16>
 hipError_t attend_d(const KvView &c, const AttendPlan &p, const AttendArgs &a, bool weigh, hipStream_t s) {
   if (p.lone) {
@@ -584,11 +622,10 @@ hipError_t attend_d(const KvView &c, const AttendPlan &p, const AttendArgs &a, b
   const int chunks = weigh ? (p.len_cap + kWeighSlots - 1) / kWeighSlots : 0;
   const int64_t grid = (int64_t)c.nseq * a.hq + (int64_t)chunks * c.nseq * c.hkv;
   if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
-  if (weigh) k_kv4_attend<D, F16, true, kWaves, false><<<kShares<D>, kThreads, 0, s>>>(c, p, a);
-  else k_kv4_attend<D, F16, false, kWaves, false><<<kShares<D>, kThreads, 0, s>>>(c, p, a);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = weigh ? attend_shares<D, F16, true>(c, p, a, s) : attend_shares<D, F16, false>(c, p, a, s);
   if (e != hipSuccess) return e;
-  k_kv4_join<D, F16><<<(unsigned)grid, kThreads, 0, s>>>(c, p, a, c.nseq * a.hq, chunks);
+  if (weigh) k_kv4_join<D, F16, true><<<(unsigned)grid, kThreads, 0, s>>>(c, p, a, c.nseq * a.hq, chunks);
+  else k_kv4_join<D, F16, false><<<(unsigned)grid, kThreads, 0, s>>>(c, p, a, c.nseq * a.hq, chunks);
   return hipGetLastError();
 }
 

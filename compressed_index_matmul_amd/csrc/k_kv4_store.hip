@@ -21,10 +21,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Smallest / largest, NaN if either is.
-__device__ __forceinline__ float min_nan(float a, float b) { return __builtin_elementwise_minimum(a, b); }
-__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
-
 // The lane's neighbours in its four: lane ^ 1, lane ^ 2.
 __device__ __forceinline__ float quad_xor1(float v) {
   const int u = __float_as_int(v);
