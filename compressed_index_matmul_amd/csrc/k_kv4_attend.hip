@@ -411,6 +411,15 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
     const uint4_t pw = {pack16<true>(P[0][0], P[0][1]), pack16<true>(P[0][2], P[0][3]),
                         pack16<true>(P[1][0], P[1][1]), pack16<true>(P[1][2], P[1][3])};
     const half8_t pf = __builtin_bit_cast(half8_t, pw);
+    // fp16 results are as exact as the rounding of P: its remainder takes part too (bf16 results are not).
+    half8_t pr;
+    if (F16) {
+      float R[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) R[i] = P[i / 4][i & 3] - (float)pf[i];
+      pr = __builtin_bit_cast(half8_t, uint4_t{pack16<true>(R[0], R[1]), pack16<true>(R[2], R[3]),
+                                               pack16<true>(R[4], R[5]), pack16<true>(R[6], R[7])});
+    }
 
     half2_t sv[4], mv[4];
 #pragma unroll
@@ -428,6 +437,10 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
                               code_hi(k, w1) * sv[2] + mv[2], code_hi(k, w1 >> 8) * sv[3] + mv[3]);
       acc[2 * i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, pf, acc[2 * i], 0, 0, 0);
       acc[2 * i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, pf, acc[2 * i + 1], 0, 0, 0);
+      if (F16) {
+        acc[2 * i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, pr, acc[2 * i], 0, 0, 0);
+        acc[2 * i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, pr, acc[2 * i + 1], 0, 0, 0);
+      }
     }
     if (more) cur.load_values(next_v, next_vs, lane);
   }
