@@ -180,7 +180,7 @@ def _output(out, like, dev, own):
     """`out`, checked, or a new tensor of `like`'s shape and type; its address."""
     if out is not None:
         return out, _array(out, like.shape, like.dtype, dev, "out")
-    out = torch.empty(like.shape, dtype=like.dtype, device=dev)
+    out = torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype, device=dev)
     own.append(out)
     return out, out.data_ptr()
 

@@ -146,7 +146,7 @@ struct PromptOut {
 // SPLIT: the workgroup takes one piece of its keys and leaves its sums in the
 // workspace for k_attn_join.
 template <int D, int BN, bool F16, bool CAUSAL, bool SPLIT>
-__global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 1) void k_attn_prompt(AttnView a, PromptOut o, int tiles,
+__global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attn_prompt(AttnView a, PromptOut o, int tiles,
                                                                             int pieces) {
   constexpr int NS = BN / 32, ND = D / 32, NK = D / 16;
   __shared__ __attribute__((aligned(1024))) uint16_t s_k[2][BN * D];
@@ -244,24 +244,30 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 1) void k_attn_prompt(Attn
     if (k0 <= lim_last) {
       const uint32_t ks = ka + (t & 1) * (BN * D * 2), vs = va + (t & 1) * (BN * D * 2);
       float16_t S[NS];
-      uint4_t kf[2][NK];
+      // the keys' pieces in the order of their products, kAhead of them read ahead
+      constexpr int kAhead = D == 256 ? 4 : NK < 8 ? NK : 8, kAll = NS * NK;
+      uint4_t kf[kAhead];
+      auto read_k = [&](int x) {
+        const int n = x / NK, i = x % NK;
+        return lds_read((ks ^ (i & 7) * 32) + n * 64 * D + (i >> 3) * 256);
+      };
 #pragma unroll
-      for (int i = 0; i < NK; ++i) kf[0][i] = lds_read((ks ^ (i & 7) * 32) + (i >> 3) * 256);
+      for (int x = 0; x < kAhead; ++x) kf[x] = read_k(x);
       sched_fence();
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) S[n][r] = 0.0f;
+      }
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-          if (n + 1 < NS) kf[(n + 1) & 1][i] = lds_read((ks ^ (i & 7) * 32) + (n + 1) * 64 * D + (i >> 3) * 256);
-          S[n] = mfma32<F16>(kf[n & 1][i], qf[i], S[n]);
-        }
+      for (int x = 0; x < kAll; ++x) {
+        S[x / NK] = mfma32<F16>(kf[x % kAhead], qf[x % NK], S[x / NK]);
+        if (x + kAhead < kAll) kf[x % kAhead] = read_k(x + kAhead);
+      }
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-          if (n + 1 < NS) sched_group<0x100, 1>();
-          sched_group<0x008, 1>();
-        }
+      for (int x = 0; x < kAll; ++x) {
+        sched_group<0x008, 1>();
+        if (x + kAhead < kAll) sched_group<0x100, 1>();
       }
       sched_fence();
       if (k0 + BN - 1 > lim_first) {
@@ -297,16 +303,16 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 1) void k_attn_prompt(Attn
           part[r & 3] += S[n][r];
         }
       lsum += (part[0] + part[1]) + (part[2] + part[3]);
-      uint4_t vf[2][ND];
-      auto read_v = [&](uint4_t *v, int st) {
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          const uint32_t p = (vs ^ (d & 3) * 64) + 32 * st * D + (d >> 2) * 256;
-          const uint2_t v0 = lds_column(p), v1 = lds_column(p + 16 * D);
-          v[d] = uint4_t{v0[0], v0[1], v1[0], v1[1]};
-        }
+      constexpr int kVAhead = (ND < 4 ? ND : 4), kVAll = 2 * NS * ND;
+      uint4_t vf[kVAhead];
+      auto read_v = [&](int x) {
+        const int st = x / ND, d = x % ND;
+        const uint32_t p = (vs ^ (d & 3) * 64) + 32 * st * D + (d >> 2) * 256;
+        const uint2_t v0 = lds_column(p), v1 = lds_column(p + 16 * D);
+        return uint4_t{v0[0], v0[1], v1[0], v1[1]};
       };
-      read_v(vf[0], 0);
+#pragma unroll
+      for (int x = 0; x < kVAhead; ++x) vf[x] = read_v(x);
       uint4_t pf[2 * NS];
 #pragma unroll
       for (int st = 0; st < 2 * NS; ++st)
@@ -314,15 +320,14 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 1) void k_attn_prompt(Attn
         for (int i = 0; i < 4; ++i) pf[st][i] = pack16<F16>(S[st / 2][8 * (st & 1) + 2 * i], S[st / 2][8 * (st & 1) + 2 * i + 1]);
       sched_fence();
 #pragma unroll
-      for (int st = 0; st < 2 * NS; ++st) {
-        if (st + 1 < 2 * NS) read_v(vf[(st + 1) & 1], st + 1);
+      for (int x = 0; x < kVAll; ++x) {
+        acc[x % ND] = mfma32<F16>(vf[x % kVAhead], pf[x / ND], acc[x % ND]);
+        if (x + kVAhead < kVAll) vf[x % kVAhead] = read_v(x + kVAhead);
+      }
 #pragma unroll
-        for (int d = 0; d < ND; ++d) acc[d] = mfma32<F16>(vf[st & 1][d], pf[st], acc[d]);
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          if (st + 1 < 2 * NS) sched_group<0x100, 2>();
-          sched_group<0x008, 1>();
-        }
+      for (int x = 0; x < kVAll; ++x) {
+        sched_group<0x008, 1>();
+        if (x + kVAhead < kVAll) sched_group<0x100, 2>();
       }
       sched_fence();
     }
