@@ -404,17 +404,14 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnView a, PromptOut o,
   const int seen = a.causal ? min(q0 + kRows + rk.n - rq.n, rk.n) : rk.n;
   const int nt = seen > 0 ? (seen + BN - 1) / BN : 0;
   const int64_t step = (int64_t)a.tq * a.hq;
+  const int per = max((nt + pieces - 1) / pieces, kMinKeys / BN), np = (nt + per - 1) / per;  // as piece_tiles
   float top = -INFINITY;
-  int np = 0;
-  for (; np < pieces; ++np) {
-    int t0, t1;
-    piece_tiles(nt, pieces, np, BN, &t0, &t1);
-    if (t0 >= t1) break;
-    top = fmaxf(top, o.stat[(np * step + at) * 2]);
-  }
+#pragma unroll 4
+  for (int p = 0; p < np; ++p) top = fmaxf(top, o.stat[(p * step + at) * 2]);
   const float m0 = top == -INFINITY ? 0.0f : top;
   float4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
   float l = 0.0f;
+#pragma unroll 4
   for (int p = 0; p < np; ++p) {
     const float2_t st = *reinterpret_cast<const float2_t *>(o.stat + (p * step + at) * 2);
     const float4_t v = *reinterpret_cast<const float4_t *>(o.part + (p * step + at) * D + d);

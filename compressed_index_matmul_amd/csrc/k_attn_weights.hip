@@ -143,6 +143,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights_join(const float *__r
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= n) return;
   float sum = 0.0f;
+#pragma unroll 8
   for (int p = 0; p < pieces; ++p) sum += part[p * n + i];
   weights[i] = accumulate ? weights[i] + sum : sum;
 }

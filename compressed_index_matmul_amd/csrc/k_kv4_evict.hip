@@ -29,7 +29,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix of a per-wave count over the workgroup's waves.
+// Exclusive prefix over the workgroup's waves of a count each wave holds.
 __device__ __forceinline__ int wave_prefix(int *s, int wave, int count) {
   __syncthreads();
   if ((threadIdx.x & 63) == 0) s[wave] = count;
@@ -125,11 +125,11 @@ __global__ __launch_bounds__(NT) void k_kv4_select(KvView c, EvictPlan p, const 
                                                             int keep, int recent, uint32_t *__restrict__ keys_all,
                                                             int32_t *__restrict__ moves, int32_t *__restrict__ counts) {
   constexpr int kSelThreads = NT, kSelWaves = NT / kWave;
-  __shared__ int s_hist[kSelWaves / 4][kCopies][256];
+  constexpr int kHist = kSelWaves / 4 * kCopies * 256;
+  __shared__ int s_hist[2][kHist];  // one fills while the other is cleared
   __shared__ int s_sum[256];
-  __shared__ int s_wave[kSelWaves];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
+  __shared__ int s_wave[kSelWaves], s_holes[kSelWaves];
+  __shared__ int s_moved;
   __shared__ int s_to[FUSE ? kFuseMoves : 1], s_from[FUSE ? kFuseMoves : 1];
 
   const int row = blockIdx.x;
@@ -180,58 +180,70 @@ __global__ __launch_bounds__(NT) void k_kv4_select(KvView c, EvictPlan p, const 
     for (int i0 = 0; i0 < steps; i0 += kBatch) load(i0);
   }
 
+  // Four digits of 8 bits from the top; `prefix` holds the digits found so far, `need` how many of the keys that have
+  // them are kept.  Every wave reads the counts and finds the digit itself: two barriers a round.
   uint32_t prefix = 0;
   int need = keep;
-  int *hist = s_hist[wave / 4][lane % kCopies];
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < kSelWaves / 4 * kCopies * 256; i += kSelThreads) (&s_hist[0][0][0])[i] = 0;
-    __syncthreads();
+  for (int i = tid; i < kHist; i += kSelThreads) s_hist[0][i] = 0;
+  __syncthreads();
+  bool all = false;  // every key with the digits so far is kept: the rest need not be known
+#pragma unroll
+  for (int round = 0; round < 4; ++round) {
+    const int shift = 24 - 8 * round;
+    if (all) continue;
+    int *hist = &s_hist[round & 1][(wave / 4 * kCopies + lane % kCopies) * 256];
     each_step<R>(steps, first, [&](int i, int slot) {
       if (slot < len) {
         const uint32_t key = keys.get(i, ws, slot);
-        if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255u], 1);
+        if (round == 0 || (key >> (shift + 8 & 31)) == (prefix >> (shift + 8 & 31))) atomicAdd(&hist[(key >> shift) & 255u], 1);
       }
     });
     __syncthreads();
     if (tid < 256) {
       int n = 0;
 #pragma unroll
-      for (int w = 0; w < kSelWaves / 4 * kCopies; ++w) n += (&s_hist[0][0][0])[w * 256 + tid];
+      for (int w = 0; w < kSelWaves / 4 * kCopies; ++w) n += s_hist[round & 1][w * 256 + tid];
       s_sum[tid] = n;
     }
+    if (round < 3)
+      for (int i = tid; i < kHist; i += kSelThreads) s_hist[~round & 1][i] = 0;
     __syncthreads();
-    if (wave == 0) {  // digits from the top: the one that holds the need-th key
-      int n[4], mine = 0;
+    int n[4], mine = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n[i] = s_sum[255 - 4 * lane - i], mine += n[i];
-      int upto = mine;  // inclusive prefix over the lanes
+    for (int i = 0; i < 4; ++i) n[i] = s_sum[255 - 4 * lane - i], mine += n[i];
+    int upto = mine;  // inclusive prefix over the lanes
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(upto, o);
-        if (lane >= o) upto += v;
-      }
-      int above = upto - mine;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (above < need && need <= above + n[i]) {
-          s_prefix = prefix | (uint32_t)(255 - 4 * lane - i) << shift;
-          s_need = need - above;
-        }
-        above += n[i];
-      }
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o);
+      if (lane >= o) upto += v;
     }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
+    int above = upto - mine, digit = -1, left = 0, count = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (above < need && need <= above + n[i]) digit = 255 - 4 * lane - i, left = need - above, count = n[i];
+      above += n[i];
+    }
+    const int at = __builtin_ctzll(__ballot(digit >= 0));  // one lane holds it
+    prefix |= (uint32_t)__builtin_amdgcn_readlane(digit, at) << shift;
+    need = __builtin_amdgcn_readlane(left, at);
+    all = need == __builtin_amdgcn_readlane(count, at);
+    // s_sum is written again only after the next round's first barrier
   }
+  // kept: keys above `limit`, and the first `need` of those equal to it (none where whole digits are kept; a prefix of
+  // zero cannot be passed by one less, and keeps all its keys as ties)
+  const uint32_t limit = all && prefix > 0 ? prefix - 1 : prefix;
+  if (all) need = prefix > 0 ? 0 : len;
 
   // ties of the keep-th key by slot, then the two lists
   const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
-  int ties = 0;
-  each_step<R>(steps, first, [&](int i, int slot) {
-    ties += __popcll(__ballot(slot < len && keys.get(i, ws, min(slot, len - 1)) == prefix));
-  });
-  const int ties_before = wave_prefix(s_wave, wave, ties);
+  int ties_before = 0;
+  if (need > 0) {
+    int ties = 0;
+    each_step<R>(steps, first, [&](int i, int slot) {
+      ties += __popcll(__ballot(slot < len && keys.get(i, ws, min(slot, len - 1)) == limit));
+    });
+    ties_before = wave_prefix(s_wave, wave, ties);
+  }
   int holes_at = 0, movers_at = 0;
   int32_t *to = moves + (int64_t)row * 2 * p.max_moves, *from = to + p.max_moves;
 #pragma unroll
@@ -240,8 +252,8 @@ __global__ __launch_bounds__(NT) void k_kv4_select(KvView c, EvictPlan p, const 
     each_step<R>(steps, first, [&](int i, int slot) {
       const bool in = slot < len;
       const uint32_t key = keys.get(i, ws, min(slot, len - 1));
-      const uint64_t tie = __ballot(in && key == prefix);
-      const bool stays = in && (key > prefix || (key == prefix && t + __popcll(tie & below) < need));
+      const uint64_t tie = __ballot(in && key == limit);
+      const bool stays = in && (key > limit || (key == limit && t + __popcll(tie & below) < need));
       t += __popcll(tie);
       const bool is_hole = in && !stays && slot < keep, is_mover = stays && slot >= keep;
       const uint64_t hole = __ballot(is_hole), mover = __ballot(is_mover);
@@ -254,10 +266,11 @@ __global__ __launch_bounds__(NT) void k_kv4_select(KvView c, EvictPlan p, const 
       m += __popcll(mover);
     });
     if (pass == 0) {
-      holes_at = wave_prefix(s_wave, wave, h);
+      if (lane == 0) s_holes[wave] = h;
       movers_at = wave_prefix(s_wave, wave, m);
+      for (int i = 0; i < wave; ++i) holes_at += s_holes[i];
       if (wave == kSelWaves - 1 && lane == 0) {
-        if (FUSE) s_need = movers_at + m;
+        if (FUSE) s_moved = movers_at + m;
         else counts[row] = movers_at + m;
       }
     }
@@ -265,7 +278,7 @@ __global__ __launch_bounds__(NT) void k_kv4_select(KvView c, EvictPlan p, const 
   if (FUSE) {
     __syncthreads();
     const int i = tid / kMoveLanes;
-    if (i < s_need) move_slot<FUSE ? FUSE : 64>(c, b, kvh, s_from[i], s_to[i], lane % kMoveLanes);
+    if (i < s_moved) move_slot<FUSE ? FUSE : 64>(c, b, kvh, s_from[i], s_to[i], lane % kMoveLanes);
   }
 }
 
