@@ -186,56 +186,70 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 struct Line {
   int64_t total, share;
   int rows;
+  uint32_t n, upto;  // of the lane's sequence among the first 64: tiles, and their sum up to it
 };
-__device__ __forceinline__ uint32_t prefix64(uint32_t v) {  // inclusive, over the wave
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t u = __shfl_up(v, o);
-    if (lane >= o) v += u;
-  }
+// Inclusive sum over the lanes of the wave.
+__device__ __forceinline__ uint32_t prefix64(uint32_t v) {
+#define VQMM_ADD_DPP(ctrl, rows) v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xF, false)
+  VQMM_ADD_DPP(0x111, 0xF);  // row_shr 1, 2, 4, 8: within 16 lanes
+  VQMM_ADD_DPP(0x112, 0xF);
+  VQMM_ADD_DPP(0x114, 0xF);
+  VQMM_ADD_DPP(0x118, 0xF);
+  VQMM_ADD_DPP(0x142, 0xA);  // lane 15 of a row to the next one (rows 1 and 3)
+  VQMM_ADD_DPP(0x143, 0xC);  // lane 31 to the upper half
+#undef VQMM_ADD_DPP
   return v;
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); }
+// Tiles of the 64 sequences from b0 on (64 of below 2^26: their sum is within 32 bits).
+__device__ __forceinline__ uint32_t tiles64(const KvView &c, const AttendPlan &p, int b0) {
+  const int b = b0 + (threadIdx.x & 63);
+  return b < c.nseq ? (uint32_t)tiles_of(c, p, b) : 0u;
 }
 template <int D, bool WEIGH>
 __device__ __forceinline__ Line line_of(const KvView &c, const AttendPlan &p) {
-  const int lane = threadIdx.x & 63;
-  int64_t sum = 0;
-  for (int b0 = 0; b0 < c.nseq; b0 += 64) {
-    const uint32_t n = b0 + lane < c.nseq ? tiles_of(c, p, b0 + lane) : 0;  // 64 of below 2^26: within 32 bits
-    sum += (uint32_t)__builtin_amdgcn_readlane((int)prefix64(n), 63);
-  }
   Line l;
+  l.n = tiles64(c, p, 0);
+  l.upto = prefix64(l.n);
+  int64_t sum = lane_value(l.upto, 63);
+  for (int b0 = 64; b0 < c.nseq; b0 += 64) sum += lane_value(prefix64(tiles64(c, p, b0)), 63);
   l.rows = c.hkv * p.htiles;
   l.total = sum * l.rows;
   const int64_t even = (l.total + kShares<D, WEIGH> - 1) / kShares<D, WEIGH>;
   l.share = max((even + kWaves - 1) / kWaves * kWaves, (int64_t)kWaves);
   return l;
 }
-// The sequence that holds position pos < total, and where it begins.
-__device__ __forceinline__ int line_find(const KvView &c, const AttendPlan &p, const Line &l, int64_t pos, int64_t *begin) {
-  const int lane = threadIdx.x & 63;
+// The sequence that holds position pos < total, where it begins and its tiles.
+__device__ __forceinline__ int line_find(const KvView &c, const AttendPlan &p, const Line &l, int64_t pos, int64_t *begin,
+                                         int *tiles) {
   int64_t base = 0;
+  uint32_t n = l.n, upto = l.upto;
   for (int b0 = 0;; b0 += 64) {
-    const uint32_t n = b0 + lane < c.nseq ? tiles_of(c, p, b0 + lane) : 0;
-    const uint32_t upto = prefix64(n);
     const uint64_t past = __ballot(base + (int64_t)upto * l.rows > pos);
     if (past || b0 + 64 >= c.nseq) {
       const int at = past ? __builtin_ctzll(past) : 63;
-      *begin = base + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)(upto - n), at) * l.rows;
+      *tiles = (int)lane_value(n, at);
+      *begin = base + (int64_t)(lane_value(upto, at) - lane_value(n, at)) * l.rows;
       return min(b0 + at, c.nseq - 1);
     }
-    base += (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)upto, 63) * l.rows;
+    base += (int64_t)lane_value(upto, 63) * l.rows;
+    n = tiles64(c, p, b0 + 64);
+    upto = prefix64(n);
   }
 }
-// Where sequence b begins.
-__device__ __forceinline__ int64_t line_begin(const KvView &c, const AttendPlan &p, const Line &l, int b) {
-  const int lane = threadIdx.x & 63;
+// Where sequence b begins, and its tiles.
+__device__ __forceinline__ int64_t line_begin(const KvView &c, const AttendPlan &p, const Line &l, int b, int *tiles) {
   int64_t base = 0;
-  for (int b0 = 0; b0 < b; b0 += 64) {
-    const uint32_t n = b0 + lane < b ? tiles_of(c, p, b0 + lane) : 0;
-    base += (uint32_t)__builtin_amdgcn_readlane((int)prefix64(n), 63);
+  uint32_t n = l.n, upto = l.upto;
+  for (int b0 = 0;; b0 += 64) {
+    if (b < b0 + 64) {
+      *tiles = (int)lane_value(n, b - b0);
+      return base + (int64_t)(lane_value(upto, b - b0) - lane_value(n, b - b0)) * l.rows;
+    }
+    base += (int64_t)lane_value(upto, 63) * l.rows;
+    n = tiles64(c, p, b0 + 64);
+    upto = prefix64(n);
   }
-  return base * l.rows;
 }
 
 // LONE: a workgroup of NW waves a row, all of it.
@@ -272,8 +286,7 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
     pos = pos_end;
   } else {
     int64_t begin;
-    b = __builtin_amdgcn_readfirstlane(line_find(c, p, line, pos, &begin));
-    ntiles = __builtin_amdgcn_readfirstlane(tiles_of(c, p, b));
+    b = __builtin_amdgcn_readfirstlane(line_find(c, p, line, pos, &begin, &ntiles));
     const int in = (int)(pos - begin);  // a sequence's tiles over all rows are below 2^31
     row = __builtin_amdgcn_readfirstlane(in / ntiles);
     t_begin = __builtin_amdgcn_readfirstlane(in - row * ntiles);
@@ -502,12 +515,17 @@ struct Parts {
 };
 template <int D>
 __device__ __forceinline__ Parts parts_of(const KvView &c, const AttendPlan &p, const Line &l, int b, int row) {
-  const int nt = tiles_of(c, p, b);
-  const int64_t begin = line_begin(c, p, l, b) + (int64_t)row * nt, end = begin + nt;
+  int nt;
+  const int64_t begin = line_begin(c, p, l, b, &nt) + (int64_t)row * nt, end = begin + nt;
   Parts r;
   r.empty = nt == 0;
-  r.first = (int)(begin / l.share);
-  r.n = nt == 0 ? 0 : (int)((end - 1) / l.share) - r.first + 1;
+  if (l.total < ((int64_t)1 << 31)) {  // short divisions, nearly always
+    r.first = (int)begin / (int)l.share;
+    r.n = nt == 0 ? 0 : (int)(end - 1) / (int)l.share - r.first + 1;
+  } else {
+    r.first = (int)(begin / l.share);
+    r.n = nt == 0 ? 0 : (int)((end - 1) / l.share) - r.first + 1;
+  }
   r.whole = r.n == 1;
   return r;
 }
@@ -549,8 +567,8 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
   if ((int)blockIdx.x < out_blocks) {
     constexpr int kSub = kThreads / (D / 4);  // parts summed side by side, four channels a thread
     __shared__ float s_part[kSub][D];
+    const int b = (int)blockIdx.x / a.hq, head = (int)blockIdx.x - b * a.hq;
     const int64_t at = blockIdx.x;
-    const int b = (int)(at / a.hq), head = (int)(at - (int64_t)b * a.hq);
     const int kvh = head / p.group, ht = (head - kvh * p.group) / 16, h = (head - kvh * p.group) % 16;
     const Parts parts = parts_of<D>(c, p, line, b, kvh * p.htiles + ht);
     if (parts.whole) return;
