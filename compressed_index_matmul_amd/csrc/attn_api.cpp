@@ -109,13 +109,16 @@ int check_rows(const KvView &v, int32_t total, const int32_t *cu) {
 int check_attend_sizes(const KvView &v, int n_q_heads, int max_len) {
   if (n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % v.hkv != 0 || max_len < 0) return VQ_ERR_SHAPE;
   const int64_t group = n_q_heads / v.hkv;
-  const int64_t rows = v.hkv * ((group + 15) / 16);
+  const int64_t rows = v.hkv * ((group + 15) / 16);  // of a sequence
+  if (((int64_t)max_len / 1024 + 1) * v.nseq * v.hkv + (int64_t)v.nseq * n_q_heads > kMaxInt) return VQ_ERR_SHAPE;
   if (v.nseq * rows > ((int64_t)1 << 22) || ((int64_t)max_len / 32 + 1) * rows > kMaxInt) return VQ_ERR_SHAPE;
   return VQ_OK;
 }
 
 int check_evict_sizes(const KvView &v, int keep, int recent, int max_len) {
-  if (keep < 1 || max_len < 0 || (int64_t)v.nseq * v.hkv > ((int64_t)1 << 22)) return VQ_ERR_SHAPE;
+  if (keep < 1 || max_len < 0) return VQ_ERR_SHAPE;
+  const int64_t rows = (int64_t)v.nseq * v.hkv, moves = std::max(0, std::min(keep, max_len - keep));
+  if (rows > ((int64_t)1 << 22) || rows * (moves / 16 + 1) > kMaxInt) return VQ_ERR_SHAPE;
   if (recent < 0 || recent > keep) return VQ_ERR_VALUE;
   return VQ_OK;
 }

@@ -5,7 +5,13 @@
 // as one operand of 32x32x16 MFMA; the queries of the group's heads pass through
 // double-buffered LDS.  S = Q K^T puts a key in a lane's column and 16 queries in
 // its registers, so the sum over queries needs no exchange until the end, and
-// one workgroup sees all the queries of its keys: no atomics, a fixed order.
+// one workgroup sees all the queries of its keys (or a piece of them, where key
+// blocks are few; pieces meet in a second launch): no atomics, a fixed order.
+//
+// Bound: exponentials, one a pair, next to 2 head_dim flops on the matrix
+// cores.  7620 keys of three prompts against their last 64 queries, 32/8 heads
+// of 128: 14 us, mostly the latency of four rounds; every query of 2048 + 701,
+// 9/3 heads of 64: 15 + 4 us.
 #include "attn_device.h"
 
 #include <algorithm>
