@@ -37,85 +37,12 @@ constexpr int kThreads = 256;
 constexpr int kRows = 128;  // queries of a workgroup
 constexpr float kSlack = 8.0f;
 
-template <bool F16>
-__device__ __forceinline__ float16_t mfma32(uint4_t a, uint4_t b, float16_t c) {
-  if (F16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
-}
-
-// LDS by byte address.
-typedef __attribute__((address_space(3))) uint4_t lds_uint4;
 typedef __attribute__((address_space(3))) short4_t lds_short4;
-__device__ __forceinline__ uint4_t lds_read(uint32_t at) { return *(lds_uint4 *)at; }
 // Four 16-bit values of one column, rows 0..3 of a 4 x 16 block in LDS whose
 // row r, columns 4 j .. 4 j + 3 the lane 4 r + j of the 16 points at.
 __device__ __forceinline__ uint2_t lds_column(uint32_t at) {
-  return __builtin_bit_cast(uint2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)at));
+  return __builtin_bit_cast(uint2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)at));
 }
-
-// Tiles of BN rows go from global memory straight into LDS, 16 bytes a lane, a
-// wave's 64 pieces next to one another: no registers, no LDS writes to issue.
-// Rows are not padded; instead the 16-byte pieces of a row are permuted by an
-// XOR with bits of the row, in the address each lane loads from:
-//   keys   : piece ^ (row & 15) (D = 64: row / 2 & 7): 16 rows of one piece,
-//            a quarter of a b128 read
-//   values : piece ^ 4 (row & 3) (D = 64: 4 (row / 2 & 1)): the 64-byte spans
-//            that the transposing reads take from 4 rows
-// fall on different banks (64 of 4 bytes).
-template <int D>
-__device__ __forceinline__ int key_swizzle(int row) {
-  return D == 64 ? (row >> 1) & 7 : row & 15;
-}
-template <int D>
-__device__ __forceinline__ int value_swizzle(int row) {
-  return D == 64 ? (row & 2) << 1 : (row & 3) << 2;
-}
-
-__device__ __forceinline__ uint32_t lds_address(const void *p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
-}
-
-// 16 bytes a lane from base + off to LDS at `lds` + 16 lane (m0; nothing else here
-// uses it).  Not waited for:
-// wait_loads() before the barrier that publishes the tile.
-__device__ __forceinline__ void load_to_lds(uint32_t lds, const char *base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-               : "memory");
-}
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-template <int D, int BN>
-struct Stage {
-  static constexpr int kRowsPerLoad = 512 / D;                    // rows of a wave's 1024 bytes
-  static constexpr int kLoads = BN / (4 * kRowsPerLoad);          // of a wave and tile
-  // the lane's row of the tile for the wave's first load, and its piece in the
-  // even and in the odd loads (4 kRowsPerLoad rows apart)
-  uint32_t row, piece[2];
-  __device__ __forceinline__ Stage(int wave, int lane, bool value) {
-    row = kRowsPerLoad * wave + lane / (D / 8);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = row + i * 4 * kRowsPerLoad;
-      piece[i] = (lane % (D / 8)) ^ (value ? value_swizzle<D>(r) : key_swizzle<D>(r));
-    }
-  }
-  // rows row0 .. row0 + BN - 1 of n (those past the end repeat the last one)
-  __device__ __forceinline__ void load(uint32_t lds, const uint16_t *base, int64_t ts, int row0, int n, int wave) const {
-    lds += wave * 1024;
-    const char *p = reinterpret_cast<const char *>(base + row0 * ts);
-    if (row0 + BN <= n) {
-      const uint32_t off = row * (uint32_t)ts * 2u;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        load_to_lds(lds + i * 4096, p + (int64_t)i * (4 * kRowsPerLoad) * ts * 2, off + piece[i & 1] * 16u);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        load_to_lds(lds + i * 4096, p, (uint32_t)min((int)row + i * 4 * kRowsPerLoad, n - 1 - row0) * (uint32_t)ts * 2u + piece[i & 1] * 16u);
-    }
-  }
-};
 
 // Infinities and NaN among the eight values of a 16-byte piece become zeros;
 // returns whether there were any.

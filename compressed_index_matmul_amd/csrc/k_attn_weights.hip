@@ -3,7 +3,7 @@
 //
 // A workgroup owns 128 keys of one key/value head, 32 a wave, held in registers
 // as one operand of 32x32x16 MFMA; the queries of the group's heads pass through
-// double-buffered LDS.  S = Q K^T puts a key in a lane's column and 16 queries in
+// double-buffered LDS, straight from global memory.  S = Q K^T puts a key in a lane's column and 16 queries in
 // its registers, so the sum over queries needs no exchange until the end, and
 // one workgroup sees all the queries of its keys (or a piece of them, where key
 // blocks are few; pieces meet in a second launch): no atomics, a fixed order.
@@ -23,19 +23,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kKeys = 128;
 
-template <bool F16>
-__device__ __forceinline__ float16_t mfma32(uint4_t a, uint4_t b, float16_t c) {
-  if (F16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
-}
-
 template <int D, int BQ, bool F16, bool CAUSAL>
 __global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const float *__restrict__ lse, int last,
                                                            int accumulate, float *__restrict__ weights, int pieces) {
-  constexpr int QP = 8, NK = D / 16, NQ = BQ / 32;
-  constexpr int kPieces = BQ * (D / 8) / kThreads;
-  __shared__ __attribute__((aligned(16))) uint16_t s_q[2][BQ * (D + QP)];
+  constexpr int NK = D / 16, NQ = BQ / 32;
+  __shared__ __attribute__((aligned(1024))) uint16_t s_q[2][BQ * D];
   __shared__ __attribute__((aligned(16))) float s_lse[2][BQ];
 
   const int kvh = blockIdx.x % a.hkv;
@@ -67,55 +59,49 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const flo
   const int it0 = (int)((int64_t)items * piece / pieces), it1 = (int)((int64_t)items * (piece + 1) / pieces);
   const float cs = a.scale * kLog2e;
 
-  // Two query tiles in flight: a tile's loads go out two rounds before it is
-  // wanted, into one of two register sets, and into LDS one barrier before.
-  struct Stage {
-    uint4_t r[kPieces];
-    float lse;
-  };
-  auto fetch = [&](Stage &st, int it) {
+  const Stage<D, BQ> sq(wave, lane, false);
+  const uint32_t lq = lds_address(s_q);
+  // piece 2 i + h of the lane's query row, at qa ^ 32 i (256 bytes on from i = 8)
+  const uint32_t qa = lq + col * (2 * D) + (h ^ key_swizzle<D>(col)) * 16;
+  float next_lse = 0.0f;
+  auto fetch = [&](int it) {
     const int head = kvh * group + it / ni, r0 = low + it % ni * BQ;
-    const uint16_t *qp = a.q + rq.begin * a.q_ts + head * a.q_hs;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int id = threadIdx.x + i * kThreads, row = r0 + id / (D / 8);
-      st.r[i] = uint4_t{0, 0, 0, 0};
-      if (row < rq.n) st.r[i] = *reinterpret_cast<const uint4_t *>(qp + row * a.q_ts + id % (D / 8) * 8);
-    }
     if (threadIdx.x < BQ) {
-      // rows past the end, and rows without keys, give exp2(-inf) = 0
       const int row = r0 + threadIdx.x;
-      const float v = row < rq.n ? lse[(int64_t)head * a.tq + rq.begin + row] : -INFINITY;
-      st.lse = v == -INFINITY ? INFINITY : v * kLog2e;
+      next_lse = row < rq.n ? lse[(int64_t)head * a.tq + rq.begin + row] : -INFINITY;
     }
+    sq.load(lq + (it & 1) * (BQ * D * 2), a.q + rq.begin * a.q_ts + head * a.q_hs, a.q_ts, r0, rq.n, wave);
+  };
+  auto publish = [&](int it) {
+    // rows past the end, and rows of nothing but -inf, give exp2(-inf) = 0
+    if (threadIdx.x < BQ) s_lse[it & 1][threadIdx.x] = next_lse == -INFINITY ? INFINITY : next_lse * kLog2e;
+    wait_loads();
+    __syncthreads();
   };
   float sum = 0.0f;
-  auto step = [&](Stage &st, int it) {
-    const int buf = it & 1;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int id = threadIdx.x + i * kThreads;
-      *reinterpret_cast<uint4_t *>(&s_q[buf][(id / (D / 8)) * (D + QP) + id % (D / 8) * 8]) = st.r[i];
-    }
-    if (threadIdx.x < BQ) s_lse[buf][threadIdx.x] = st.lse;
-    __syncthreads();
-    if (it + 2 < it1) fetch(st, it + 2);
+  if (it0 < it1) {
+    fetch(it0);
+    publish(it0);
+  }
+  for (int it = it0; it < it1; ++it) {
+    if (it + 1 < it1) fetch(it + 1);
     const int r0 = low + it % ni * BQ;
-    if (CAUSAL && r0 + BQ - 1 + off < kw) return;  // no query of the tile sees a key of the wave
-    const bool mask = r0 + BQ > rq.n || (CAUSAL && r0 + off < kw + 31);
+    const uint32_t qs = qa + (it & 1) * (BQ * D * 2);
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
+      const int rw = r0 + 32 * n;
+      if (rw >= rq.n || (CAUSAL && rw + 31 + off < kw)) continue;  // none of these queries sees a key of the wave
+      const bool mask = rw + 32 > rq.n || (CAUSAL && rw + off < kw + 31);
       float16_t S;
 #pragma unroll
       for (int r = 0; r < 16; ++r) S[r] = 0.0f;
-      const uint16_t *qs = &s_q[buf][(32 * n + col) * (D + QP) + 8 * h];
 #pragma unroll
-      for (int i = 0; i < NK; ++i) S = mfma32<F16>(*reinterpret_cast<const uint4_t *>(qs + 16 * i), kf[i], S);
+      for (int i = 0; i < NK; ++i) S = mfma32<F16>(lds_read((qs ^ (i & 7) * 32) + n * 64 * D + (i >> 3) * 256), kf[i], S);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int q8 = 32 * n + 8 * x + 4 * h;
-        const float4_t l4 = *reinterpret_cast<const float4_t *>(&s_lse[buf][q8]);
+        const float4_t l4 = *reinterpret_cast<const float4_t *>(&s_lse[it & 1][q8]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float p = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * x + i], cs, -l4[i]));
@@ -128,13 +114,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const flo
       }
     }
     sum += (part[0] + part[1]) + (part[2] + part[3]);
-  };
-  Stage st0, st1;
-  if (it0 < it1) fetch(st0, it0);
-  if (it0 + 1 < it1) fetch(st1, it0 + 1);
-  for (int it = it0; it < it1; it += 2) {
-    step(st0, it);
-    if (it + 1 < it1) step(st1, it + 1);
+    if (it + 1 < it1) publish(it + 1);
   }
   sum = sum_xor32(sum);
   if (h == 0 && ki < rk.n) {
@@ -174,14 +154,18 @@ hipError_t weights_d(const AttnView &a, const PromptPlan &p, const float *lse, i
 }  // namespace
 
 // Few key blocks (less than one and a half a CU) are cut along the queries,
-// into about 1536 workgroups of at least one tile: under a causal mask the
-// first keys have the most queries, so pieces also even the work out.
+// into about 1536 workgroups of at least one tile, and long runs of queries
+// into pieces of about 64 tiles: under a causal mask the first keys have the
+// most queries, so pieces also even the work out (8191 + 2000 tokens of 32/8
+// heads, 648 key blocks: one piece took 841 us, five @GB@).
 PromptPlan attn_weights_plan(const AttnView &a, int last) {
   PromptPlan p{1, 0, 0};
-  const int64_t blocks = ((int64_t)a.tk / kKeys + a.nseq) * a.hkv;
-  const int64_t queries = last > 0 ? std::min(last, a.tq) : a.tq;
-  const int64_t most = (queries + 63) / 64 * (a.hq / a.hkv);
-  if (blocks > 0 && blocks < 384 && most > 1) p.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({1536 / blocks, most, 32}));
+  const int64_t blocks = ((int64_t)a.tk / kKeys + a.nseq) * a.hkv, group = a.hq / a.hkv;
+  const int64_t mean = a.nseq > 0 ? ((int64_t)a.tq + a.nseq - 1) / a.nseq : 0;
+  const int64_t most = ((last > 0 ? std::min(last, a.tq) : a.tq) + 63) / 64 * group;
+  const int64_t run = ((last > 0 ? std::min<int64_t>(last, mean) : mean) + 63) / 64 * group;
+  const int64_t want = std::max<int64_t>(blocks > 0 && blocks < 384 ? 1536 / blocks : 1, (run + 63) / 64);
+  p.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 32}));
   if (p.pieces > 1) p.bytes = (size_t)p.pieces * a.hkv * a.tk * 4;
   return p;
 }

@@ -154,7 +154,8 @@ __global__ __launch_bounds__(NT) void k_kv4_select(KvView c, EvictPlan p, const 
   // Keys in the order of the weights, protected slots on top; what lanes past
   // the end hold counts nowhere.
   Keys<R> keys;
-  const int tiles = c.ps / 32;
+  // 32-slot tile t is on page t / tiles: exact by one multiplication for t < 2^26 and tiles <= 32
+  const uint32_t tiles = c.ps / 32, inverse = tiles > 1 ? 0xffffffffu / tiles + 1 : 0;
   constexpr int kBatch = 8;  // steps whose loads go out together
   auto load = [&](int i0) {
     int64_t at[kBatch];
@@ -162,7 +163,7 @@ __global__ __launch_bounds__(NT) void k_kv4_select(KvView c, EvictPlan p, const 
     float w[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int slot = min(first + (i0 + j) * kWave, len - 1), pi = (slot >> 5) / tiles;
+      const int slot = min(first + (i0 + j) * kWave, len - 1), pi = tiles > 1 ? (int)__umulhi(slot >> 5, inverse) : slot >> 5;
       at[j] = (page_of(c, b, pi) * c.hkv + kvh) * c.ps + (slot - pi * c.ps);
     }
 #pragma unroll
