@@ -38,7 +38,8 @@ COMMON_FLAGS = [
 # Device code generation of single sources.  k_attn_prompt: the output sums stay in vector registers; in accumulation
 # registers each rescale would copy them out and back, and the copies end up in every round of the loop (heads of 256:
 # 115 against 89 us for a chunk of 512 queries on 4609 keys).
-SOURCE_FLAGS = {"k_attn_prompt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# k_attn_weights likewise: its scores go on to vector instructions at once.
+SOURCE_FLAGS = {s: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for s in ("k_attn_prompt.hip", "k_attn_weights.hip")}
 
 
 def hipcc() -> str:

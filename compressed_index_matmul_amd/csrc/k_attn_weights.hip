@@ -100,18 +100,21 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const flo
       for (int i = 0; i < NK; ++i) S = mfma32<F16>(lds_read((qs ^ (i & 7) * 32) + n * 64 * D + (i >> 3) * 256), kf[i], S);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int q8 = 32 * n + 8 * x + 4 * h;
-        const float4_t l4 = *reinterpret_cast<const float4_t *>(&s_lse[it & 1][q8]);
+        const float4_t l4 = *reinterpret_cast<const float4_t *>(&s_lse[it & 1][32 * n + 8 * x + 4 * h]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float p = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * x + i], cs, -l4[i]));
-          if (mask) {
-            const int row = r0 + q8 + i;
-            p = row < rq.n && (!CAUSAL || ki <= row + off) ? p : 0.0f;
-          }
-          part[i] += p;
+        for (int i = 0; i < 4; ++i) S[4 * x + i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * x + i], cs, -l4[i]));
+      }
+      if (mask) {
+        asm volatile("");  // a branch, not selects in every tile
+        const int from = max(CAUSAL ? ki - off : 0, 0) - rw - 4 * h, to = rq.n - rw - 4 * h;  // the queries that count
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int q = 8 * (r / 4) + (r & 3);
+          S[r] = q >= from && q < to ? S[r] : 0.0f;
         }
       }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) part[r & 3] += S[r];
     }
     sum += (part[0] + part[1]) + (part[2] + part[3]);
     if (it + 1 < it1) publish(it + 1);
