@@ -67,6 +67,60 @@ def test_chunks_and_rows_without_keys(vq, d, causal):
     one(vq, "fp16", 4, 2, d, [40, 100, 33, 7, 0, 130], [300, 60, 0, 8, 50, 129], causal=causal, seed=1)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hkv,d", [(3, 1, 64), (4, 2, 128), (2, 1, 256)])
+def test_few_rows_against_many_keys(vq, hq, hkv, d, kind):
+    """Keys in pieces: the call asks for a workspace; rows of long, short and
+    no keys side by side; the workspace may hold anything."""
+    import torch
+    from compressed_index_matmul_amd.attention import AttnBatch
+    b = AttnBatch(1, hq, hkv, d, 4, 218, 3030, 1, 0.1, 0, None, None)
+    need = vq.lib().attn_prompt_workspace_size(b)
+    assert need > 0
+    lens, klens = [130, 1, 80, 7], [2500, 300, 230, 0]
+    for causal in (True, False):
+        out, lse = one(vq, kind, hq, hkv, d, lens, klens, causal=causal, seed=d, last=(0, 20))
+    rng = np.random.default_rng(d)
+    cu, cu_d = offsets(lens)
+    ck, ck_d = offsets(klens)
+    q, _ = heads(rng, cu[-1], hq, d, kind)
+    k, _ = heads(rng, ck[-1], hkv, d, kind)
+    want, l1 = vq.attn_prompt(q, k, k, cu_d, ck_d, return_lse=True)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    got, l2 = vq.attn_prompt(q, k, k, cu_d, ck_d, return_lse=True, workspace=ws)
+    assert torch.equal(got, want) and torch.equal(l1, l2)
+    with pytest.raises(vq.VQError) as e:
+        vq.attn_prompt(q, k, k, cu_d, ck_d, workspace=ws[:need - 16])
+    assert e.value.status == -8
+    # a value that is not finite, in the last piece, reaches the queries that see it and no other
+    v = k.clone()
+    v[2500 - 100, 0, 7] = float("inf")
+    got = vq.attn_prompt(q, k, v, cu_d, ck_d)
+    sees = 130 - 100  # the first query of the first sequence that sees that key
+    group = hq // hkv
+    assert torch.equal(got[:sees], vq.attn_prompt(q, k, k, cu_d, ck_d)[:sees])
+    assert bool((got[sees:130, :group, 7] == float("inf")).all()) and bool(torch.isfinite(got[sees:130, :, 8:]).all())
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (2, 2, 128), (1, 1, 256)])
+def test_many_tiles(vq, hq, hkv, d):
+    """Long enough for dozens of tiles, with keys whose scores grow along the
+    sequence, so that the running maximum moves all the time."""
+    import torch
+    rng = np.random.default_rng(d)
+    n = 1500
+    cu, cu_d = offsets([n])
+    ramp = torch.linspace(0.1, 6.0, n)[:, None, None]
+    q, q64 = heads(rng, n, hq, d, "bf16")
+    k = (torch.from_numpy(rng.standard_normal((n, hkv, d)).astype(np.float32)) * ramp).bfloat16()
+    v, v64 = heads(rng, n, hkv, d, "bf16")
+    k64, k = k.double().numpy(), k.cuda()
+    out, lse = vq.attn_prompt(q, k, v, cu_d, return_lse=True)
+    ref, lref, mag, vsum, smag = oa.prompt_ref(q64, k64, v64, cu, cu, d ** -0.5, True)
+    check(lse, lref, oa.lse_bound(lref, smag, d, n), "lse")
+    check(out, ref, oa.prompt_bound(ref, mag, vsum, smag, d, n, "bf16"), "out")
+
+
 def test_empty_batches(vq):
     import torch
     q = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device="cuda")

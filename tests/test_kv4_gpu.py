@@ -204,6 +204,25 @@ def test_attend_splits(vq, n):
     attend(vq, "fp16", 4, 1, 64, 64, [n, 3, 0, 129], seed=n + 1)
 
 
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (6, 3), (20, 1)])
+def test_attend_many_sequences(vq, hq, hkv):
+    """More sequences than a wave has lanes, empty ones among them, longer than
+    one workgroup takes whole."""
+    rng = np.random.default_rng(hq)
+    lens = [int(n) for n in rng.integers(0, 90, 150)]
+    for i in (0, 63, 64, 65, 127, 128, 149):
+        lens[i] = 0
+    lens[70] = 1100
+    attend(vq, "bf16", hq, hkv, 64, 32, lens, seed=hq)
+
+
+def test_attend_many_long_rows(vq):
+    """More rows than shares and rows longer than one: whole rows, rows cut
+    once and rows cut often in the same call."""
+    attend(vq, "fp16", 2, 1, 64, 128, [1500, 40, 1200, 0, 64, 2000], seed=21)
+    attend(vq, "bf16", 8, 8, 128, 64, [1300, 33], seed=22)
+
+
 def test_attend_max_len(vq):
     """Lengths beyond max_len count as max_len."""
     attend(vq, "bf16", 4, 2, 64, 32, [300, 10, 200], seed=4, max_len=190, caps=190)
@@ -423,6 +442,14 @@ def test_evict_weights(vq, make):
 def test_evict_long(vq):
     """Thousands of slots, and a length that is no multiple of anything."""
     evict(vq, 1, 64, 256, [40001, 3], 5000, 100, RANDOM, seed=3)
+
+
+@pytest.mark.parametrize("n,keep", [(2048, 2040), (2049, 2040), (5000, 700), (5000, 4990), (16384, 100), (16385, 4000),
+                                    (32768, 32760), (32769, 32750), (33000, 9000)])
+def test_evict_sizes(vq, n, keep):
+    """Both sides of the lengths at which the search changes its form, with
+    few and with many slots to move."""
+    evict(vq, 1, 64, 128, [n, keep + 1, 5], keep, min(50, keep), RANDOM, seed=n)
 
 
 def test_evict_max_len_and_nothing_to_do(vq):
