@@ -8,10 +8,11 @@
 // one workgroup sees all the queries of its keys (or a piece of them, where key
 // blocks are few; pieces meet in a second launch): no atomics, a fixed order.
 //
-// Bound: exponentials, one a pair, next to 2 head_dim flops on the matrix
-// cores.  7620 keys of three prompts against their last 64 queries, 32/8 heads
-// of 128: 14 us, mostly the latency of four rounds; every query of 2048 + 701,
-// 9/3 heads of 64: 15 + 4 us.
+// Bound: vector issue (an exponential, a fused multiply-add and an add a pair)
+// next to 2 head_dim flops on the matrix cores.  Every query of 8191 + 2000
+// tokens, 32/8 heads of 128: 309 us, 0.94 PFLOP/s.  7620 keys of three prompts
+// against their last 64 queries: 12.8 us, mostly the latency of four rounds;
+// every query of 2048 + 701, 9/3 heads of 64: 11.3 + 4.0 us.
 #include "attn_device.h"
 
 #include <algorithm>
@@ -160,7 +161,7 @@ hipError_t weights_d(const AttnView &a, const PromptPlan &p, const float *lse, i
 // into about 1536 workgroups of at least one tile, and long runs of queries
 // into pieces of about 64 tiles: under a causal mask the first keys have the
 // most queries, so pieces also even the work out (8191 + 2000 tokens of 32/8
-// heads, 648 key blocks: one piece took 841 us, five @GB@).
+// heads, 648 key blocks: one piece took 841 us, five 447 us).
 PromptPlan attn_weights_plan(const AttnView &a, int last) {
   PromptPlan p{1, 0, 0};
   const int64_t blocks = ((int64_t)a.tk / kKeys + a.nseq) * a.hkv, group = a.hq / a.hkv;
