@@ -15,7 +15,7 @@
 // out in batches of eight, and where no more than 16 slots can move (a step's
 // own eviction) the selecting workgroup moves them and the second launch is
 // saved.  Eight sequences of up to 8191 slots of 8 heads of 128 down to 1024:
-// 17.9 + 8.1 us; one slot over 1024 in 32 sequences: 8.0 us.
+// 16.4 + 8.2 us; one slot over 1024 in 32 sequences: 8.0 us.
 #include "attn_device.h"
 
 #include <algorithm>
@@ -43,6 +43,11 @@ __device__ __forceinline__ int wave_prefix(int *s, int wave, int count) {
   int before = 0;
   for (int i = 0; i < wave; ++i) before += s[i];
   return before;
+}
+
+// Set bits of a wave's mask at the lanes below.
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
 // Copies slot src to slot dst, by the 16 lanes l of one move: keys and values
@@ -149,7 +154,7 @@ __global__ __launch_bounds__(NT) void k_kv4_select(KvView c, EvictPlan p, const 
   uint32_t *ws = keys_all + (int64_t)row * p.len_cap;
   const int64_t oldest = (int64_t)next_pos[b] - recent;  // positions from here on are kept
   const int steps = (len + kSelThreads - 1) / kSelThreads;
-  const int first = wave * steps * kWave + lane;
+  const int first = wave * steps * kWave + lane;  // (wave: uniform)
 
   // Keys in the order of the weights, protected slots on top; what lanes past
   // the end hold counts nowhere.
@@ -242,7 +247,6 @@ __global__ __launch_bounds__(NT) void k_kv4_select(KvView c, EvictPlan p, const 
   if (all) need = prefix > 0 ? 0 : len;
 
   // ties of the keep-th key by slot, then the two lists
-  const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
   int ties_before = 0;
   if (need > 0) {
     int ties = 0;
@@ -253,24 +257,38 @@ __global__ __launch_bounds__(NT) void k_kv4_select(KvView c, EvictPlan p, const 
   }
   int holes_at = 0, movers_at = 0;
   int32_t *to = moves + (int64_t)row * 2 * p.max_moves, *from = to + p.max_moves;
+  uint32_t kept = 0;  // bit i: the lane's slot of step i stays (keys in registers)
 #pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
     int t = ties_before, h = holes_at, m = movers_at;
     each_step<R>(steps, first, [&](int i, int slot) {
+      const int s0 = first - lane + i * kWave;  // the step's first slot, the same for the wave
       const bool in = slot < len;
-      const uint32_t key = keys.get(i, ws, min(slot, len - 1));
-      const uint64_t tie = __ballot(in && key == limit);
-      const bool stays = in && (key > limit || (key == limit && t + __popcll(tie & below) < need));
-      t += __popcll(tie);
-      const bool is_hole = in && !stays && slot < keep, is_mover = stays && slot >= keep;
-      const uint64_t hole = __ballot(is_hole), mover = __ballot(is_mover);
-      if (pass == 1) {
-        const int hi = h + __popcll(hole & below), mi = m + __popcll(mover & below);
-        if (is_hole) FUSE ? s_to[hi] = slot : to[hi] = slot;
-        if (is_mover) FUSE ? s_from[mi] = slot : from[mi] = slot;
+      bool stays;
+      if (R > 0 && pass == 1) {
+        stays = (kept >> (i & 31)) & 1u;
+      } else {
+        const uint32_t key = keys.get(i, ws, min(slot, len - 1));
+        stays = in && key > limit;
+        if (need > 0) {
+          const uint64_t tie = __ballot(in && key == limit);
+          stays = stays || (in && key == limit && lanes_below(tie) + t < need);
+          t += __popcll(tie);
+        }
+        if (R > 0) kept |= (uint32_t)stays << (i & 31);
       }
-      h += __popcll(hole);
-      m += __popcll(mover);
+      if (s0 < keep) {
+        const bool is = in && !stays && slot < keep;
+        const uint64_t hole = __ballot(is);
+        if (pass == 1 && is) (FUSE ? s_to : to)[h + lanes_below(hole)] = slot;
+        h += __popcll(hole);
+      }
+      if (s0 + kWave > keep) {
+        const bool is = stays && slot >= keep;
+        const uint64_t mover = __ballot(is);
+        if (pass == 1 && is) (FUSE ? s_from : from)[m + lanes_below(mover)] = slot;
+        m += __popcll(mover);
+      }
     });
     if (pass == 0) {
       if (lane == 0) s_holes[wave] = h;
