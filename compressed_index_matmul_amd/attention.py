@@ -93,6 +93,11 @@ def _pkg():
 
 _FN = {}
 
+# The current stream's handle and the current device without building Python
+# objects (2 us a call); the public calls where this torch has no such names.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
 
 def _fn(name):
     f = _FN.get(name)
@@ -106,13 +111,13 @@ def _call(name, dev, stream, own, *args):
     call allocated, kept from reuse until the stream is done with them."""
     fn = _FN.get(name) or _fn(name)
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+        handle = _raw_stream(dev.index)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
         for t in own:
             t.record_stream(st)
-    if torch._C._cuda_getDevice() == dev.index:
+    if _current_device() == dev.index:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):

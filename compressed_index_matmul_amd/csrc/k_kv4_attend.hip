@@ -177,6 +177,7 @@ struct AttendArgs {
   float *stat;    // [share][2][16][2]: maximum (log2 domain), sum
   float *whole;   // [seq][head][2]: the same of rows that one share covers (add_weights)
   float *score;   // [seq][head][pitch], log2 domain (add_weights)
+  int64_t *begins;  // [seq + 1]: tiles of one row before each sequence
 };
 
 __device__ __forceinline__ int tiles_of(const KvView &c, const AttendPlan &p, int b) {
@@ -192,7 +193,11 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 struct Line {
   int64_t total, share;
   int rows;
-  uint32_t n, upto;  // of the lane's sequence among the first 64: tiles, and their sum up to it
+  // the 64 sequences that the search has come to: the first of them, where it
+  // begins, and of the lane's sequence the tiles and their sum up to it
+  int b0;
+  int64_t base;
+  uint32_t n, upto;
 };
 // Inclusive sum over the lanes of the wave.
 __device__ __forceinline__ uint32_t prefix64(uint32_t v) {
@@ -212,49 +217,52 @@ __device__ __forceinline__ uint32_t tiles64(const KvView &c, const AttendPlan &p
   const int b = b0 + (threadIdx.x & 63);
   return b < c.nseq ? (uint32_t)tiles_of(c, p, b) : 0u;
 }
+// Shares of equal size, in whole rounds of a workgroup's waves.
 template <int D, bool WEIGH>
-__device__ __forceinline__ Line line_of(const KvView &c, const AttendPlan &p) {
+__device__ __forceinline__ int64_t share_of(int64_t total) {
+  const int64_t even = (total + kShares<D, WEIGH> - 1) / kShares<D, WEIGH>;
+  return max((even + kWaves - 1) / kWaves * kWaves, (int64_t)kWaves);
+}
+// The whole line; the first workgroup leaves where each sequence begins (in
+// tiles of one row), and the end, for k_kv4_join.
+template <int D, bool WEIGH>
+__device__ __forceinline__ Line line_of(const KvView &c, const AttendPlan &p, int64_t *begins) {
   Line l;
   l.n = tiles64(c, p, 0);
   l.upto = prefix64(l.n);
+  const bool leave = blockIdx.x == 0 && threadIdx.x < 64;
+  if (leave && (int)threadIdx.x < c.nseq) begins[threadIdx.x] = l.upto - l.n;
   int64_t sum = lane_value(l.upto, 63);
-  for (int b0 = 64; b0 < c.nseq; b0 += 64) sum += lane_value(prefix64(tiles64(c, p, b0)), 63);
+#pragma unroll 4
+  for (int b0 = 64; b0 < c.nseq; b0 += 64) {
+    const uint32_t n = tiles64(c, p, b0), upto = prefix64(n);
+    if (leave && b0 + (int)threadIdx.x < c.nseq) begins[b0 + threadIdx.x] = sum + (upto - n);
+    sum += lane_value(upto, 63);
+  }
+  if (leave && threadIdx.x == 0) begins[c.nseq] = sum;
   l.rows = c.hkv * p.htiles;
   l.total = sum * l.rows;
-  const int64_t even = (l.total + kShares<D, WEIGH> - 1) / kShares<D, WEIGH>;
-  l.share = max((even + kWaves - 1) / kWaves * kWaves, (int64_t)kWaves);
+  l.share = share_of<D, WEIGH>(l.total);
+  l.b0 = 0;
+  l.base = 0;
   return l;
 }
-// The sequence that holds position pos < total, where it begins and its tiles.
-__device__ __forceinline__ int line_find(const KvView &c, const AttendPlan &p, const Line &l, int64_t pos, int64_t *begin,
+// The sequence that holds position pos < total, no earlier than the last one
+// found; where it begins and its tiles.
+__device__ __forceinline__ int line_find(const KvView &c, const AttendPlan &p, Line &l, int64_t pos, int64_t *begin,
                                          int *tiles) {
-  int64_t base = 0;
-  uint32_t n = l.n, upto = l.upto;
-  for (int b0 = 0;; b0 += 64) {
-    const uint64_t past = __ballot(base + (int64_t)upto * l.rows > pos);
-    if (past || b0 + 64 >= c.nseq) {
+  for (;;) {
+    const uint64_t past = __ballot(l.base + (int64_t)l.upto * l.rows > pos);
+    if (past || l.b0 + 64 >= c.nseq) {
       const int at = past ? __builtin_ctzll(past) : 63;
-      *tiles = (int)lane_value(n, at);
-      *begin = base + (int64_t)(lane_value(upto, at) - lane_value(n, at)) * l.rows;
-      return min(b0 + at, c.nseq - 1);
+      *tiles = (int)lane_value(l.n, at);
+      *begin = l.base + (int64_t)(lane_value(l.upto, at) - lane_value(l.n, at)) * l.rows;
+      return min(l.b0 + at, c.nseq - 1);
     }
-    base += (int64_t)lane_value(upto, 63) * l.rows;
-    n = tiles64(c, p, b0 + 64);
-    upto = prefix64(n);
-  }
-}
-// Where sequence b begins, and its tiles.
-__device__ __forceinline__ int64_t line_begin(const KvView &c, const AttendPlan &p, const Line &l, int b, int *tiles) {
-  int64_t base = 0;
-  uint32_t n = l.n, upto = l.upto;
-  for (int b0 = 0;; b0 += 64) {
-    if (b < b0 + 64) {
-      *tiles = (int)lane_value(n, b - b0);
-      return base + (int64_t)(lane_value(upto, b - b0) - lane_value(n, b - b0)) * l.rows;
-    }
-    base += (int64_t)lane_value(upto, 63) * l.rows;
-    n = tiles64(c, p, b0 + 64);
-    upto = prefix64(n);
+    l.base += (int64_t)lane_value(l.upto, 63) * l.rows;
+    l.b0 += 64;
+    l.n = tiles64(c, p, l.b0);
+    l.upto = prefix64(l.n);
   }
 }
 
@@ -271,7 +279,7 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
   Line line{};
   int64_t pos = 0, pos_end = 1;
   if (!LONE) {
-    line = line_of<D, WEIGH>(c, p);
+    line = line_of<D, WEIGH>(c, p, a.begins);
     line.total = uniform(line.total);
     line.share = uniform(line.share);
     pos = blockIdx.x * line.share;
@@ -519,18 +527,17 @@ struct Parts {
   int first, n;
   bool whole, empty;
 };
-template <int D>
-__device__ __forceinline__ Parts parts_of(const KvView &c, const AttendPlan &p, const Line &l, int b, int row) {
-  int nt;
-  const int64_t begin = line_begin(c, p, l, b, &nt) + (int64_t)row * nt, end = begin + nt;
+__device__ __forceinline__ Parts parts_of(const AttendArgs &a, int64_t total, int64_t share, int rows, int b, int row) {
+  const int nt = (int)(a.begins[b + 1] - a.begins[b]);
+  const int64_t begin = a.begins[b] * rows + (int64_t)row * nt, end = begin + nt;
   Parts r;
   r.empty = nt == 0;
-  if (l.total < ((int64_t)1 << 31)) {  // short divisions, nearly always
-    r.first = (int)begin / (int)l.share;
-    r.n = nt == 0 ? 0 : (int)(end - 1) / (int)l.share - r.first + 1;
+  if (total < ((int64_t)1 << 31)) {  // short divisions, nearly always
+    r.first = (int)begin / (int)share;
+    r.n = nt == 0 ? 0 : (int)(end - 1) / (int)share - r.first + 1;
   } else {
-    r.first = (int)(begin / l.share);
-    r.n = nt == 0 ? 0 : (int)((end - 1) / l.share) - r.first + 1;
+    r.first = (int)(begin / share);
+    r.n = nt == 0 ? 0 : (int)((end - 1) / share) - r.first + 1;
   }
   r.whole = r.n == 1;
   return r;
@@ -569,14 +576,15 @@ constexpr int kWeighSlots = kThreads * 4;  // slots of a workgroup of the weight
 // sequence and key/value head.
 template <int D, bool F16, bool WEIGH>
 __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, AttendArgs a, int out_blocks, int chunks) {
-  const Line line = line_of<D, WEIGH>(c, p);
+  const int rows = c.hkv * p.htiles;
+  const int64_t total = a.begins[c.nseq] * rows, share = share_of<D, WEIGH>(total);
   if ((int)blockIdx.x < out_blocks) {
     constexpr int kSub = kThreads / (D / 4);  // parts summed side by side, four channels a thread
     __shared__ float s_part[kSub][D];
     const int b = (int)blockIdx.x / a.hq, head = (int)blockIdx.x - b * a.hq;
     const int64_t at = blockIdx.x;
     const int kvh = head / p.group, ht = (head - kvh * p.group) / 16, h = (head - kvh * p.group) % 16;
-    const Parts parts = parts_of<D>(c, p, line, b, kvh * p.htiles + ht);
+    const Parts parts = parts_of(a, total, share, rows, b, kvh * p.htiles + ht);
     if (parts.whole) return;
     float top, sum;
     head_stats(a, parts, at, h, &top, &sum);
@@ -615,7 +623,7 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
   for (int ht = 0; ht < p.htiles; ++ht) {  // heads of the group, 16 at a time
     const int ng = min(16, p.group - ht * 16);
     const int64_t at0 = (int64_t)b * a.hq + kvh * p.group + ht * 16;
-    const Parts parts = parts_of<D>(c, p, line, b, kvh * p.htiles + ht);
+    const Parts parts = parts_of(a, total, share, rows, b, kvh * p.htiles + ht);
     __syncthreads();
     for (int g = wave; g < ng; g += kWaves) {
       float top, sum;
@@ -681,7 +689,8 @@ AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add
   auto round = [](size_t x) { return (x + 255) & ~(size_t)255; };
   const size_t pieces = (size_t)shares_of(c.d) * 2 * 16, heads = (size_t)c.nseq * n_q_heads;
   p.stat_off = round(pieces * c.d * 4);
-  p.whole_off = p.stat_off + round(pieces * 8);
+  p.begin_off = p.stat_off + round(pieces * 8);
+  p.whole_off = p.begin_off + round(((size_t)c.nseq + 1) * 8);
   p.score_off = p.whole_off + (add_weights ? round(heads * 8) : 0);
   p.bytes = p.score_off + (add_weights ? round(heads * p.score_pitch * 4) : 0);
   return p;
@@ -693,7 +702,7 @@ hipError_t launch_kv4_attend(const KvView &c, const AttendPlan &p, const void *q
   char *w = static_cast<char *>(ws);
   AttendArgs a{q,   q_ts, q_hs, scale, n_q_heads, out, lse, reinterpret_cast<float *>(w),
                reinterpret_cast<float *>(w + p.stat_off), reinterpret_cast<float *>(w + p.whole_off),
-               reinterpret_cast<float *>(w + p.score_off)};
+               reinterpret_cast<float *>(w + p.score_off), reinterpret_cast<int64_t *>(w + p.begin_off)};
   if (c.d == 64) return f16 ? attend_d<64, true>(c, p, a, add_weights, s) : attend_d<64, false>(c, p, a, add_weights, s);
   if (c.d == 128)
     return f16 ? attend_d<128, true>(c, p, a, add_weights, s) : attend_d<128, false>(c, p, a, add_weights, s);

@@ -136,7 +136,7 @@ struct AttendPlan {
   bool lone;        // short and few rows: one workgroup of more waves takes each whole
   int len_cap;      // lengths are clamped to this
   int score_pitch;  // floats per head of stored scores (add_weights)
-  size_t stat_off, whole_off, score_off, bytes;
+  size_t stat_off, begin_off, whole_off, score_off, bytes;
 };
 AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add_weights);
 hipError_t launch_kv4_attend(const KvView &c, const AttendPlan &p, const void *q, int64_t q_ts, int64_t q_hs, bool f16,
