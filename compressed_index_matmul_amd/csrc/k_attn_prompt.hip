@@ -16,8 +16,9 @@
 // rescale of O.
 //
 // Bound: the matrix cores and, sharing each SIMD's issue with them, the vector
-// work of the softmax (75 instructions a lane for 32 keys, 16 of them
-// exponentials, against 16 products of 32 cycles).  Waves overlap the two, so
+// work of the softmax (about 100 instructions a lane for 32 keys, 16 of
+// them exponentials, against 16 products of 32 cycles; matrix cores 60% busy).
+// Waves overlap the two, so
 // tiles are as small as it takes to hold three waves a SIMD for heads of 128
 // (BN = 32), four for 64 (BN = 64) and two for 256 (BN = 32): 64 keys and two
 // waves took 751 us where 32 and three took 731.  Under this load the clock falls to
@@ -117,7 +118,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attn_prompt(Attn
   const int qw = q0 + wave * 32;  // the wave's first query
   const int qi = qw + col;
   const int lim = CAUSAL ? min(qi + off, rk.n - 1) : rk.n - 1;  // last key this lane's query sees
-  const int lim_first = CAUSAL ? min(qw + off, rk.n - 1) : rk.n - 1, lim_last = CAUSAL ? min(qw + 31 + off, rk.n - 1) : rk.n - 1;
+  const int lim_first = CAUSAL ? min(qw + off, rk.n - 1) : rk.n - 1;  // the same of the wave's first and last
+  const int lim_last = CAUSAL ? min(qw + 31 + off, rk.n - 1) : rk.n - 1;
   const int seen = CAUSAL ? min(q0 + kRows + off, rk.n) : rk.n;  // keys the workgroup needs
   const int all_see = CAUSAL ? min(q0 + off, rk.n - 1) : rk.n - 1;  // the last key that every query of it sees
   int t_lo = 0, nt = seen > 0 ? (seen + BN - 1) / BN : 0;

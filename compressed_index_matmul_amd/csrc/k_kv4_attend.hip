@@ -52,7 +52,8 @@ template <int D, bool WEIGH>
 constexpr int kSharesPerCu = D == 64 ? 4 : D == 128 ? (WEIGH ? 3 : 4) : 2;
 template <int D, bool WEIGH>
 constexpr int kShares = 256 * kSharesPerCu<D, WEIGH>;
-int shares_of(int d) { return d == 64 ? kShares<64, false> : d == 128 ? kShares<128, false> : kShares<256, false>; }  // the most
+// The most of them, for the workspace.
+int shares_of(int d) { return d == 64 ? kShares<64, false> : d == 128 ? kShares<128, false> : kShares<256, false>; }
 constexpr float kSlack = 8.0f;  // the reference maximum lags by up to 2^8: p <= 256 is in fp16's range
 
 // dword N of the 16 lanes of a row, in all of them.
@@ -268,7 +269,8 @@ __device__ __forceinline__ int line_find(const KvView &c, const AttendPlan &p, L
 
 // LONE: a workgroup of NW waves a row, all of it.
 template <int D, bool F16, bool WEIGH, int NW, bool LONE>
-__global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) void k_kv4_attend(KvView c, AttendPlan p, AttendArgs a) {
+__global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) void k_kv4_attend(KvView c, AttendPlan p,
+                                                                                              AttendArgs a) {
   constexpr int kThreads = NW * kWave, kWaves = NW;
   constexpr int DG = D / 32, CH = D / 16;
   constexpr int kPitch = D + 4;  // floats of a head's row in LDS: 16-byte pieces of 16 rows fall on different banks
