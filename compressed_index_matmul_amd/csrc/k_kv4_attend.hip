@@ -55,6 +55,9 @@ constexpr int kShares = 256 * kSharesPerCu<D, WEIGH>;
 // The most of them, for the workspace.
 int shares_of(int d) { return d == 64 ? kShares<64, false> : d == 128 ? kShares<128, false> : kShares<256, false>; }
 constexpr float kSlack = 8.0f;  // the reference maximum lags by up to 2^8: p <= 256 is in fp16's range
+// Beyond this reference (log2 domain) one fused multiply-add no longer does: the reference is a rounded product and its
+// rounding, 2^-24 of itself, is then many powers of two, which exp2 would send to infinity.
+constexpr float kLargeRef = 1048576.0f;
 
 // dword N of the 16 lanes of a row, in all of them.
 template <int N>
@@ -363,6 +366,7 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
 #pragma unroll
   for (int i = 0; i < CH; ++i) acc[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   float mref = -INFINITY, lsum = 0.0f;
+  bool large = false;  // some head's reference is beyond kLargeRef
 
   const int tpp = c.ps / kTile;  // tiles of a page
   const int64_t code_head = (int64_t)c.ps * (D / 2), scale_head = (int64_t)c.ps * (DG * 2);
@@ -420,21 +424,37 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
     float top = max_nan(max_nan(max_nan(S[0][0], S[0][1]), max_nan(S[0][2], S[0][3])),
                         max_nan(max_nan(S[1][0], S[1][1]), max_nan(S[1][2], S[1][3])));
     top = max_xor32(max_xor16(top)) * cs;
-    if (__any(top > mref + kSlack)) {
+    if (__any(top - mref > kSlack)) {
       const float mnew = fmaxf(mref, top);
       const float f = mnew == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mref - mnew);
       lsum *= f;
 #pragma unroll
       for (int i = 0; i < CH; ++i) acc[i] *= f;
       mref = mnew;
+      large = __any(fabsf(mref) > kLargeRef);
     }
     const float m0 = mref == -INFINITY ? 0.0f : mref;
+    if (large) {  // the product rounded as the reference's was: their difference is exact near the top
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x = S[u][i] * cs;
+          asm volatile("" : "+v"(x));  // not fused with the subtraction
+          S[u][i] = x - m0;
+        }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[u][i] = __builtin_fmaf(S[u][i], cs, -m0);
+    }
     float P[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        P[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[u][i], cs, -m0));
+        P[u][i] = __builtin_amdgcn_exp2f(S[u][i]);
         lsum += P[u][i];
       }
     const uint4_t pw = {pack16<true>(P[0][0], P[0][1]), pack16<true>(P[0][2], P[0][3]),

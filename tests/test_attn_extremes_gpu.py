@@ -1,0 +1,83 @@
+"""Attention at the ends of its range: scores far beyond what a 24-bit product
+resolves, and weight spread thinly over very many tokens."""
+import numpy as np
+import pytest
+
+import oracle.attention as oa
+from attntest import block_table, check, ints, new_cache, offsets, torch_type
+from vqtest import ensure_built
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def vq():
+    ensure_built()
+    import compressed_index_matmul_amd as m
+    m.lib()
+    return m
+
+
+def stored(vq, k, v, lens, page, seed):
+    """A cache of the packed rows; its block table on the host and the GPU, and
+    the keys and values that it stands for, float64."""
+    import torch
+    per = max(1, -(-max(lens) // page))
+    table = block_table(np.random.default_rng(seed), len(lens), per, len(lens) * per)
+    cache = new_cache(vq, table.size, page, k.shape[1], k.shape[2])
+    _, cu = offsets(lens)
+    t = torch.from_numpy(table).cuda()
+    vq.kv4_append(cache, k, v, cu, t)
+    k, v = vq.kv4_read(cache, cu, t, sum(lens), dtype=torch.float32)
+    return cache, table, t, k.double().cpu().numpy(), v.double().cpu().numpy()
+
+
+def one_query(q, k, v, lens, scale):
+    """out and lse [B, Hq], the weights [Hq, T], sum_j p_j |v_j| and sum_j |v_j|
+    of one query a sequence over packed keys and values, float64."""
+    hq, g = q.shape[1], q.shape[1] // k.shape[1]
+    out, mag, vsum = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
+    lse, p, at = np.zeros(q.shape[:2]), np.zeros((hq, k.shape[0])), 0
+    for b, n in enumerate(lens):
+        for h in range(hq):
+            kk, vv = k[at:at + n, h // g], v[at:at + n, h // g]
+            p[h, at:at + n], lse[b, h] = oa.softmax_rows(kk @ q[b, h] * scale)
+            out[b, h], mag[b, h], vsum[b, h] = p[h, at:at + n] @ vv, p[h, at:at + n] @ np.abs(vv), np.abs(vv).sum(0)
+        at += n
+    return out, lse, p, mag, vsum
+
+
+def signs(rng, n, h, d, kind, size):
+    """+-size, [n, h, d]: products of powers of two, so scores are exact in fp32."""
+    import torch
+    x = torch.from_numpy((rng.integers(0, 2, (n, h, d)) * 2.0 - 1.0) * size).to(torch_type(kind))
+    return x.cuda(), x.double().numpy()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[200, 33], [1500, 70]])
+def test_attend_scores_beyond_products(vq, lens, d, kind):
+    """Scores of 2^33 and more: the keys are a step times a code plus a minimum,
+    all with few bits, so that scores are exact in fp32 and equal ones tie; the
+    result is the mean over the largest."""
+    import torch
+    rng = np.random.default_rng(d)
+    k, _ = signs(rng, sum(lens), 2, d, "fp32", 16384.0)
+    v = torch.from_numpy(rng.standard_normal((sum(lens), 2, d)).astype(np.float32)).cuda()
+    cache, table, t, k64, v64 = stored(vq, k, v, lens, 64, d)
+    q, q64 = signs(rng, len(lens), 6, d, kind, 16384.0)
+    ref, lref, p, mag, vsum = one_query(q64, k64, v64, lens, 1.0)
+    bound = oa.prompt_bound(ref, mag, vsum, np.zeros((6, len(lens))), d, max(lens), kind, "fp16", 2.0 ** -11)
+    cache.weights.zero_()
+    for weigh in (False, True):
+        out, lse = vq.kv4_attend(q, cache, t, ints(lens), scale=1.0, add_weights=weigh, return_lse=True)
+        check(out, ref, bound, "out")
+        check(lse, lref, oa.lse_bound(lref, np.zeros_like(lref), d, max(lens)), "lse")
+    got, at = cache.weights.cpu().numpy(), 0
+    for b, n in enumerate(lens):
+        slots = np.arange(n)
+        w = got[table[b, slots // 64], :, slots % 64]
+        want = p[:, at:at + n].reshape(2, 3, n).sum(1).T
+        np.testing.assert_allclose(w, want, rtol=2.0 ** -19, atol=0)
+        at += n
