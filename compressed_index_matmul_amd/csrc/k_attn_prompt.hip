@@ -37,6 +37,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 128;  // queries of a workgroup
 constexpr float kSlack = 8.0f;
+// Beyond this reference (log2 domain) one fused multiply-add no longer does: the reference is a rounded product and its
+// rounding, 2^-24 of itself, is then many powers of two, which exp2 would send to infinity.
+constexpr float kLargeRef = 1048576.0f;
 
 typedef __attribute__((address_space(3))) short4_t lds_short4;
 // Four 16-bit values of one column, rows 0..3 of a 4 x 16 block in LDS whose
@@ -145,6 +148,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attn_prompt(Attn
   float mref = -INFINITY, lsum = 0.0f;  // in units of scores
   const float cs = a.scale * kLog2e;
   const float slack = kSlack / cs;
+  bool large = false;  // some query's reference is beyond kLargeRef
 
   const Stage<D, BN> sk(wave, lane, false), sv(wave, lane, true);
   const uint32_t lk = lds_address(s_k), lv = lds_address(s_v);
@@ -224,15 +228,24 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attn_prompt(Attn
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, S[n][r]);
       top = max_xor32(top);
-      if (__any(top > mref + slack)) {
+      if (__any(top - mref > slack)) {
         const float mnew = fmaxf(mref, top);
         const float f = mnew == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((mref - mnew) * cs);
         lsum *= f;
 #pragma unroll
         for (int i = 0; i < ND; ++i) acc[i] *= f;
         mref = mnew;
+        large = __any(fabsf(mref * cs) > kLargeRef);
       }
-      const float m0 = mref == -INFINITY ? 0.0f : mref * cs;
+      const float m = mref == -INFINITY ? 0.0f : mref;
+      if (large) {  // the difference first: exact near the top
+        asm volatile("");
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) S[n][r] -= m;
+      }
+      const float m0 = large ? 0.0f : m * cs;
       float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int n = 0; n < NS; ++n)

@@ -81,3 +81,22 @@ def test_attend_scores_beyond_products(vq, lens, d, kind):
         want = p[:, at:at + n].reshape(2, 3, n).sum(1).T
         np.testing.assert_allclose(w, want, rtol=2.0 ** -19, atol=0)
         at += n
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,klens", [([150, 33], [150, 33]), ([60], [2100])])
+def test_prompt_scores_beyond_products(vq, lens, klens, d, kind):
+    """The same for prompts, with their keys in one piece and in several:
+    scores are multiples of 2^30 up to 2^38."""
+    import torch
+    rng = np.random.default_rng(d)
+    (cu, cu_d), (ck, ck_d) = offsets(lens), offsets(klens)
+    q, q64 = signs(rng, sum(lens), 4, d, kind, 32768.0)
+    k, k64 = signs(rng, sum(klens), 2, d, kind, 32768.0)
+    v = torch.from_numpy(rng.standard_normal((sum(klens), 2, d)).astype(np.float32)).to(torch_type(kind))
+    ref, lref, mag, vsum, _ = oa.prompt_ref(q64, k64, v.double().numpy(), cu, ck, 1.0, True)
+    zero = np.zeros_like(lref)
+    out, lse = vq.attn_prompt(q, k, v.cuda(), cu_d, ck_d, scale=1.0, return_lse=True)
+    check(lse, lref, oa.lse_bound(lref, zero, d, max(klens)), "lse")
+    check(out, ref, oa.prompt_bound(ref, mag, vsum, zero, d, max(klens), kind), "out")
