@@ -100,3 +100,20 @@ def test_prompt_scores_beyond_products(vq, lens, klens, d, kind):
     out, lse = vq.attn_prompt(q, k, v.cuda(), cu_d, ck_d, scale=1.0, return_lse=True)
     check(lse, lref, oa.lse_bound(lref, zero, d, max(klens)), "lse")
     check(out, ref, oa.prompt_bound(ref, mag, vsum, zero, d, max(klens), kind), "out")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,klens", [([150, 33], [150, 33]), ([900], [40])])
+def test_gathered_weights_of_scores_beyond_products(vq, lens, klens, d, kind):
+    """And for the weights their keys gather: exp(s - lse) of a score and an
+    lse that are both multiples of large powers of two."""
+    rng = np.random.default_rng(d)
+    (cu, cu_d), (ck, ck_d) = offsets(lens), offsets(klens)
+    q, q64 = signs(rng, sum(lens), 4, d, kind, 32768.0)
+    k, k64 = signs(rng, sum(klens), 2, d, kind, 32768.0)
+    _, lse = vq.attn_prompt(q, k, k, cu_d, ck_d, scale=1.0, return_lse=True)
+    w = vq.attn_prompt_weights(q, k, lse, cu_d, ck_d, scale=1.0)
+    want, _ = oa.prompt_weights_ref(q64, k64, lse.double().cpu().numpy(), cu, ck, 1.0, True, 0)
+    assert want.max() >= 1.0
+    check(w, want, want * ((2 * max(lens) + 8) * 2.0 ** -24 + 2.0 ** -20), "weights")
