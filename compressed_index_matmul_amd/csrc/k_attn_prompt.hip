@@ -145,7 +145,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attn_prompt(Attn
   for (int i = 0; i < ND; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
-  float mref = -INFINITY, lsum = 0.0f;  // in units of scores
+  float mref = -INFINITY, m0 = 0.0f, lsum = 0.0f;  // the reference in units of scores and in the log2 domain
   const float cs = a.scale * kLog2e;
   const float slack = kSlack / cs;
   bool large = false;  // some query's reference is beyond kLargeRef
@@ -228,24 +228,25 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attn_prompt(Attn
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, S[n][r]);
       top = max_xor32(top);
-      if (__any(top - mref > slack)) {
+      if (__any(top - mref > slack) | large) {
         const float mnew = fmaxf(mref, top);
         const float f = mnew == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((mref - mnew) * cs);
         lsum *= f;
 #pragma unroll
         for (int i = 0; i < ND; ++i) acc[i] *= f;
         mref = mnew;
-        large = __any(fabsf(mref * cs) > kLargeRef);
-      }
-      const float m = mref == -INFINITY ? 0.0f : mref;
-      if (large) {  // the difference first: exact near the top
-        asm volatile("");
+        m0 = mref == -INFINITY ? 0.0f : mref * cs;
+        large = __any(fabsf(m0) > kLargeRef);
+        if (large) {  // the difference first: exact near the top
+          asm volatile("");
+          const float m = mref == -INFINITY ? 0.0f : mref;
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
+          for (int n = 0; n < NS; ++n)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) S[n][r] -= m;
+            for (int r = 0; r < 16; ++r) S[n][r] -= m;
+          m0 = 0.0f;
+        }
       }
-      const float m0 = large ? 0.0f : m * cs;
       float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int n = 0; n < NS; ++n)
