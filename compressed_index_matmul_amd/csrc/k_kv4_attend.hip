@@ -54,7 +54,11 @@ template <int D, bool WEIGH>
 constexpr int kShares = 256 * kSharesPerCu<D, WEIGH>;
 // The most of them, for the workspace.
 int shares_of(int d) { return d == 64 ? kShares<64, false> : d == 128 ? kShares<128, false> : kShares<256, false>; }
-constexpr float kSlack = 8.0f;  // the reference maximum lags by up to 2^8: p <= 256 is in fp16's range
+constexpr float kSlack = 8.0f;  // the reference maximum may lag by up to 2^8
+// Probabilities enter fp16 times 2^7, by a reference that much below the maximum it was taken from: up to 2^15 with the
+// lag, and with 11 bits down to 2^-21 of the largest.  Without it that ends at 2^-14, and below 2^-25 they are lost: where
+// one slot of 32 has a score 17 above the others', the others' part of the result was off by 4 %, at 18.5 by 95 %.
+constexpr float kRoom = 7.0f, kUnroom = 0.0078125f;
 // Beyond this reference (log2 domain) one fused multiply-add no longer does: the reference is a rounded product and its
 // rounding, 2^-24 of itself, is then many powers of two, which exp2 would send to infinity.
 constexpr float kLargeRef = 1048576.0f;
@@ -178,7 +182,7 @@ struct AttendArgs {
   void *out;
   float *lse;
   float *part;    // [share][2][16][D]: a share's part of the row it begins in, and of the one it ends in
-  float *stat;    // [share][2][16][2]: maximum (log2 domain), sum
+  float *stat;    // [share][2][16][2]: reference (log2 domain), sum
   float *whole;   // [seq][head][2]: the same of rows that one share covers (add_weights)
   float *score;   // [seq][head][pitch], log2 domain (add_weights)
   int64_t *begins;  // [seq + 1]: tiles of one row before each sequence
@@ -424,8 +428,8 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
     float top = max_nan(max_nan(max_nan(S[0][0], S[0][1]), max_nan(S[0][2], S[0][3])),
                         max_nan(max_nan(S[1][0], S[1][1]), max_nan(S[1][2], S[1][3])));
     top = max_xor32(max_xor16(top)) * cs;
-    if (__any(top - mref > kSlack)) {
-      const float mnew = fmaxf(mref, top);
+    if (__any(top - mref > kSlack + kRoom)) {
+      const float mnew = fmaxf(mref, top - kRoom);
       const float f = mnew == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mref - mnew);
       lsum *= f;
 #pragma unroll
@@ -530,7 +534,7 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
       const uint2_t w = {pack16<F16>(o[0] * r, o[1] * r), pack16<F16>(o[2] * r, o[3] * r)};
       *reinterpret_cast<uint2_t *>(static_cast<uint16_t *>(a.out) + at * D + d) = w;
       if (d == 0) {
-        if (a.lse) a.lse[at] = (__builtin_amdgcn_logf(l) + m0) * kLn2;
+        if (a.lse) a.lse[at] = (__builtin_amdgcn_logf(l * kUnroom) + (m0 + kRoom)) * kLn2;
         if (WEIGH) a.whole[at * 2] = top, a.whole[at * 2 + 1] = l;
       }
     } else {
@@ -567,7 +571,7 @@ __device__ __forceinline__ Parts parts_of(const AttendArgs &a, int64_t total, in
 __device__ __forceinline__ int64_t part_at(const Parts &r, int i, int h) {
   return ((int64_t)(r.first + i) * 2 + (i == 0 ? 1 : 0)) * 16 + h;
 }
-// Maximum and sum of one head over its parts, by one wave.
+// Reference and sum of one head over its parts, by one wave.
 __device__ __forceinline__ void head_stats(const AttendArgs &a, const Parts &r, int64_t at, int h, float *top, float *sum) {
   const int lane = threadIdx.x & 63;
   if (r.whole) {
@@ -629,7 +633,7 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
       for (int i = 0; i < kSub; ++i) y0 += s_part[i][x], y1 += s_part[i][x + 1];
       *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at * D + x) = pack16<F16>(y0 * r, y1 * r);
     }
-    if (threadIdx.x == 0 && a.lse) a.lse[at] = (__builtin_amdgcn_logf(sum) + top) * kLn2;
+    if (threadIdx.x == 0 && a.lse) a.lse[at] = (__builtin_amdgcn_logf(sum * kUnroom) + (top + kRoom)) * kLn2;
     return;
   }
   __shared__ float s_top[16], s_inv[16];

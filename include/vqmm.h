@@ -550,7 +550,10 @@ int kv4_read(const kv4_cache *c, const kv4_seqs *s, const int32_t *cu, int32_t t
  * 16-bit queries and integer codes, scaled and summed in fp32 (queries are
  * held in fp16 after a power-of-two rescale per head, exact for every value
  * within 2^28 of the head's largest); values are rounded to fp16 (relative
- * error 2^-11) and so are the probabilities, both summed in fp32.
+ * error 2^-11) and so are the probabilities, both summed in fp32.  Of a
+ * probability, relative to its head's largest, fp16 holds 11 bits down to
+ * 2^-21 and an absolute 2^-32 below; for VQ_F16 the remainder of the rounding
+ * takes part too.
  */
 int kv4_attend(const kv4_cache *c, const kv4_seqs *s, const attn_heads *q, int32_t dtype, int32_t n_q_heads,
                float scale, int32_t max_len, int32_t add_weights, void *out, float *lse, void *workspace,

@@ -117,3 +117,50 @@ def test_gathered_weights_of_scores_beyond_products(vq, lens, klens, d, kind):
     want, _ = oa.prompt_weights_ref(q64, k64, lse.double().cpu().numpy(), cu, ck, 1.0, True, 0)
     assert want.max() >= 1.0
     check(w, want, want * ((2 * max(lens) + 8) * 2.0 ** -24 + 2.0 ** -20), "weights")
+
+
+def sinks(rng, n, d, at, below, kind):
+    """Keys and values of n tokens for a query of ones with scale 1 / d: every
+    32nd token from `at` on has score 0 and value 0, the others' scores lie
+    `below` under that (spread 0.5) and their values about 1000."""
+    import torch
+    k = torch.from_numpy((rng.standard_normal((n, 1, d)) * (0.5 * d ** 0.5) - below).astype(np.float32))
+    v = torch.from_numpy((1000.0 + 100.0 * rng.standard_normal((n, 1, d))).astype(np.float32))
+    k[at::32] = 0.0
+    v[at::32] = 0.0
+    return k.to(torch_type(kind)).cuda(), v.to(torch_type(kind)).cuda()
+
+
+def thin(ref, mag, vsum, smag, largest, d, n, kind, **kw):
+    """prompt_bound for probabilities that are rounded to fp16 with room for
+    them: its 2^-24 of sum |v| allows for fp16's subnormal step of 2^-24 below
+    a largest probability of one; the largest is 2^7 at least here, so the step
+    is 2^-31 of it and its half 2^-32."""
+    return oa.prompt_bound(ref, mag, vsum * largest * 2.0 ** -8, smag, d, n, kind, **kw)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("d,n", [(64, 20000), (128, 10003), (256, 9001), (64, 1000), (256, 777)])
+@pytest.mark.parametrize("below", [17.0, 18.5])
+def test_attend_thin_weights(vq, d, n, kind, below):
+    """Some slots take nearly all the weight and give nothing; the result is
+    what the others, each of 2^-24 of the largest or less, add up to."""
+    import torch
+    rng = np.random.default_rng(d)
+    for at in (0, 31):
+        k, v = sinks(rng, n, d, at, below, "fp32")
+        cache, table, t, k64, v64 = stored(vq, k, v, [n], 256, d)
+        q = torch.ones((1, 3, d), dtype=torch_type(kind), device="cuda")
+        ref, lref, p, mag, vsum = one_query(np.ones((1, 3, d)), k64, v64, [n], 1.0 / d)
+        smag = np.full((1, 3), np.abs(k64).sum(2).max() / d)
+        bound = thin(ref, mag, vsum, smag.T, p.max(), d, n, kind, p_kind="fp16", v_round=2.0 ** -11)
+        for weigh in (False, True):
+            cache.weights.zero_()
+            out, lse = vq.kv4_attend(q, cache, t, ints([n]), scale=1.0 / d, add_weights=weigh, return_lse=True)
+            check(out, ref, bound, f"out, weigh {weigh}, at {at}")
+            check(lse, lref, oa.lse_bound(lref, smag, d, n), "lse")
+        slots = np.arange(n)
+        w = cache.weights.double().cpu().numpy()[table[0, slots // 256], 0, slots % 256]
+        want = p.sum(0)
+        rel = 2.0 * (smag[0, 0] * ((d + 8) * 2.0 ** -24 + 2.0 ** -22) + (n + 8) * 2.0 ** -24) + 2.0 ** -20
+        assert (np.abs(w - want) <= rel * want).all()
