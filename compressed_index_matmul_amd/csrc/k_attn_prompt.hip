@@ -37,6 +37,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 128;  // queries of a workgroup
 constexpr float kSlack = 8.0f;
+// fp16 probabilities are taken 2^7 larger, by a reference that much below the maximum it was taken from: up to 2^15 with
+// the lag, and with 11 bits down to 2^-21 of the largest.  Without it that ends at 2^-14, and below 2^-25 they are lost:
+// where one key of 32 has a score 17 above the others', the others' part of the result was off by 4 %, at 18.5 by 95 %.
+// bf16 has fp32's exponents.
+template <bool F16>
+constexpr float kRoom = F16 ? 7.0f : 0.0f;
+template <bool F16>
+constexpr float kUnroom = F16 ? 0.0078125f : 1.0f;
 // Beyond this reference (log2 domain) one fused multiply-add no longer does: the reference is a rounded product and its
 // rounding, 2^-24 of itself, is then many powers of two, which exp2 would send to infinity.
 constexpr float kLargeRef = 1048576.0f;
@@ -81,7 +89,7 @@ struct PromptOut {
   uint16_t *out;
   float *lse;
   float *part;  // [piece][row][head][D], sums of p v
-  float *stat;  // [piece][row][head][2]: reference maximum (log2 domain), sum of p
+  float *stat;  // [piece][row][head][2]: reference (log2 domain), sum of p
 };
 
 // SPLIT: the workgroup takes one piece of its keys and leaves its sums in the
@@ -147,7 +155,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attn_prompt(Attn
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
   float mref = -INFINITY, m0 = 0.0f, lsum = 0.0f;  // the reference in units of scores and in the log2 domain
   const float cs = a.scale * kLog2e;
-  const float slack = kSlack / cs;
+  const float room = kRoom<F16> / cs, slack = (kSlack + kRoom<F16>) / cs;
   bool large = false;  // some query's reference is beyond kLargeRef
 
   const Stage<D, BN> sk(wave, lane, false), sv(wave, lane, true);
@@ -229,7 +237,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attn_prompt(Attn
         for (int r = 0; r < 16; ++r) top = fmaxf(top, S[n][r]);
       top = max_xor32(top);
       if (__any(top - mref > slack) | large) {
-        const float mnew = fmaxf(mref, top);
+        const float mnew = fmaxf(mref, F16 ? top - room : top);
         const float f = mnew == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((mref - mnew) * cs);
         lsum *= f;
 #pragma unroll
@@ -332,8 +340,11 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attn_prompt(Attn
                          pack16<F16>(acc[d][4 * x + 2] * r, acc[d][4 * x + 3] * r)};
       *reinterpret_cast<uint2_t *>(op + 32 * d + 8 * x) = w;
     }
-  if (o.lse && h == 0)
-    o.lse[(int64_t)head * a.tq + row] = (mref == -INFINITY ? 0.0f : mref * a.scale) + __builtin_amdgcn_logf(lsum) * kLn2;
+  if (o.lse && h == 0) {
+    const float ref = mref == -INFINITY ? 0.0f : mref * cs, l2 = __builtin_amdgcn_logf(lsum * kUnroom<F16>);
+    o.lse[(int64_t)head * a.tq + row] =
+        fabsf(ref) > kLargeRef ? mref * a.scale + l2 * kLn2 : ((ref + kRoom<F16>)+l2) * kLn2;
+  }
 }
 
 // The pieces meet: D / 4 lanes take one row of one head, in piece order.
@@ -376,7 +387,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnView a, PromptOut o,
   const float r = l == 0.0f ? 0.0f : 1.0f / l;
   *reinterpret_cast<uint2_t *>(o.out + at * D + d) =
       uint2_t{pack16<F16>(sum[0] * r, sum[1] * r), pack16<F16>(sum[2] * r, sum[3] * r)};
-  if (o.lse && d == 0) o.lse[(int64_t)head * a.tq + row] = (m0 + __builtin_amdgcn_logf(l)) * kLn2;
+  if (o.lse && d == 0)
+    o.lse[(int64_t)head * a.tq + row] = ((m0 + kRoom<F16>)+__builtin_amdgcn_logf(l * kUnroom<F16>)) * kLn2;
 }
 
 template <int D, int BN, bool F16>

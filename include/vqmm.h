@@ -435,8 +435,11 @@ typedef struct attn_batch {
  *   lse : float [n_q_heads][total_q], or NULL
  * A query that sees no key gives out = 0 and lse = -inf.  Scores, the running
  * maximum and sum and the output sum are fp32; the probabilities enter the
- * second product rounded to the 16-bit type of v.  Key rows outside a
- * sequence never reach its result, whatever they hold.
+ * second product rounded to the 16-bit type of v (relative error 2^-9 for
+ * VQ_BF16; for VQ_F16 2^-12 down to 2^-21 of the row's largest, an absolute
+ * 2^-32 of it below), which leaves a 16-bit result 1.0 to 1.4 times the error
+ * of its last rounding alone.  Key rows outside a sequence never reach its
+ * result, whatever they hold.
  *   workspace : 16-byte aligned, at least attn_prompt_workspace_size bytes
  *               (NULL when that is 0): where few rows meet many keys, their
  *               keys are cut into pieces that meet in a second launch

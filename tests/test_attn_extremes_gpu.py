@@ -164,3 +164,29 @@ def test_attend_thin_weights(vq, d, n, kind, below):
         want = p.sum(0)
         rel = 2.0 * (smag[0, 0] * ((d + 8) * 2.0 ** -24 + 2.0 ** -22) + (n + 8) * 2.0 ** -24) + 2.0 ** -20
         assert (np.abs(w - want) <= rel * want).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("d,n", [(64, 20000), (128, 10003), (256, 9001), (64, 1000), (256, 777)])
+@pytest.mark.parametrize("below", [17.0, 18.5])
+def test_prompt_thin_weights(vq, d, n, kind, below):
+    """The same for prompts: a few rows against keys in pieces, and rows whose
+    keys are taken in one."""
+    import torch
+    rng = np.random.default_rng(d)
+    for at, nq in ((0, 3), (31, 700)):
+        k, v = sinks(rng, n, d, at, below, kind)
+        cu, cu_d = offsets([nq])
+        ck, ck_d = offsets([n])
+        q = torch.ones((nq, 2, d), dtype=torch_type(kind), device="cuda")
+        out, lse = vq.attn_prompt(q, k, v, cu_d, ck_d, scale=1.0 / d, causal=False, return_lse=True)
+        assert torch.equal(out[1:], out[:1].expand(nq - 1, -1, -1)) and torch.equal(lse[:, 1:], lse[:, :1].expand(-1, nq - 1))
+        k64, v64 = k.double().cpu().numpy(), v.double().cpu().numpy()
+        ref, lref, p, mag, vsum = one_query(np.ones((1, 2, d)), k64, v64, [n], 1.0 / d)
+        smag = np.full((2, 1), np.abs(k64).sum(2).max() / d)
+        if kind == "fp16":
+            bound = thin(ref, mag, vsum, smag, p.max(), d, n, kind)
+        else:
+            bound = oa.prompt_bound(ref, mag, vsum * 0.0, smag, d, n, kind)  # bf16 rounds relatively all the way down
+        check(out[:1], ref, bound, "out")
+        check(lse[:, :1], lref.T, oa.lse_bound(lref.T, smag, d, n), "lse")
