@@ -163,7 +163,6 @@ __global__ __launch_bounds__(kThreads) void k_kv4_append(KvView c, const void *_
     float hi = max_nan(max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])), max_nan(max_nan(x[4], x[5]), max_nan(x[6], x[7])));
     lo = min_nan(lo, quad_xor1(lo));
     hi = max_nan(hi, quad_xor1(hi));
-    // Saturating the ends saturates every value: one beyond them gets the code of the end, 0 or 15.
     lo = max_nan(min_nan(min_nan(lo, quad_xor2(lo)), 32768.0f), -32768.0f);
     hi = max_nan(min_nan(max_nan(hi, quad_xor2(hi)), 32768.0f), -32768.0f);
     float step = (hi - lo) * (1.0f / 15.0f);
@@ -171,11 +170,14 @@ __global__ __launch_bounds__(kThreads) void k_kv4_append(KvView c, const void *_
     const _Float16 m = (_Float16)lo, s = (_Float16)step;
     const float mf = (float)m, sf = (float)s;
     const float r = sf > 0.0f ? 1.0f / sf : 0.0f;
+    // Saturating the ends saturates every value: one beyond them gets the code of the end.  At the lower one that is 0,
+    // at the upper one 15, unless m was rounded up almost to it (fp32 only: 16-bit values are exact in m there).
+    const float most = DT == VQ_F32 ? __builtin_amdgcn_fmed3f((hi - mf) * r, 0.0f, 15.0f) : 15.0f;
     uint32_t w = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float t = (x[j] - mf) * r;  // NaN: the median is the smaller bound
-      w |= (uint32_t)__builtin_rintf(__builtin_amdgcn_fmed3f(t, 0.0f, 15.0f)) << (4 * j);
+      w |= (uint32_t)__builtin_rintf(__builtin_amdgcn_fmed3f(t, 0.0f, most)) << (4 * j);
     }
     word[i] = w;
     s16[i] = __builtin_bit_cast(uint16_t, s);

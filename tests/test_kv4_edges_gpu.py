@@ -1,0 +1,43 @@
+"""The 4-bit cache where its format ends: groups at the saturation limits, and
+what stands in them read by the decode kernel."""
+import numpy as np
+import pytest
+
+import oracle.attention as oa
+from attntest import check, heads, host_pool, ints, new_cache, offsets, torch_type
+from vqtest import ensure_built
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def vq():
+    ensure_built()
+    import compressed_index_matmul_amd as m
+    m.lib()
+    return m
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+def test_append_beside_saturation(vq, kind):
+    """Groups whose smallest value rounds up to the limit, or nearly, with
+    values beyond it: the codes are those of the saturated values."""
+    import torch
+    rng = np.random.default_rng(1)
+    rows = []
+    for low in (32767.5, 32764.0, 32760.0, 32753.0, 32752.0, 32750.0, 32700.0, 32640.0, 32000.0):
+        for big in (np.inf, 65000.0, 40000.0, 32769.0, 32768.0):
+            for end in (1.0, -1.0):
+                x = np.full(64, low) + rng.random(64) * (32768.0 - low)
+                x[rng.integers(0, 64, 20)] = big
+                x[::9] = low
+                rows.append(end * x)
+    x = torch.from_numpy(np.stack(rows).astype(np.float32)).to(torch_type(kind)).view(len(rows), 1, 64)
+    cache = new_cache(vq, 3, 32, 1, 64)
+    pool = host_pool(cache)
+    cu, cu_d = offsets([len(rows)])
+    vq.kv4_append(cache, x.cuda(), x.cuda(), cu_d, ints([[0, 2, 1]]))
+    f = x.float().numpy()
+    pool.append(f, f, cu, np.array([[0, 2, 1]], np.int32), [0])
+    np.testing.assert_array_equal(cache.codes.cpu().numpy(), pool.codes)
+    np.testing.assert_array_equal(cache.scales.cpu().numpy().view(np.uint16), pool.scales.view(np.uint16))
