@@ -86,6 +86,10 @@ __device__ __forceinline__ half2_t code_hi(const Unpack &k, uint32_t w) {
   const half2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f}, bias = {(_Float16)64.0f, (_Float16)64.0f};
   return as_h2((w & k.hi) | k.bias) * sixteenth - bias;
 }
+// What codes stand for, rounded once: 15 times the largest step, 4368, is beyond fp16 before the minimum joins it.
+__device__ __forceinline__ half2_t value(half2_t code, half2_t step, half2_t low) {
+  return __builtin_elementwise_fma(code, step, low);
+}
 __device__ __forceinline__ half8_t join(half2_t a, half2_t b, half2_t c, half2_t d) {
   return half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
@@ -484,10 +488,10 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
     for (int i = 0; i < DG; ++i) {  // two pairs of channels a word: 2 i' = CH channels in all
       const uint32_t w0 = cur.v[0].w[i], w1 = cur.v[1].w[i];
       const Unpack &k = unpack;
-      const half8_t lo = join(code_lo(k, w0) * sv[0] + mv[0], code_lo(k, w0 >> 8) * sv[1] + mv[1],
-                              code_lo(k, w1) * sv[2] + mv[2], code_lo(k, w1 >> 8) * sv[3] + mv[3]);
-      const half8_t hi = join(code_hi(k, w0) * sv[0] + mv[0], code_hi(k, w0 >> 8) * sv[1] + mv[1],
-                              code_hi(k, w1) * sv[2] + mv[2], code_hi(k, w1 >> 8) * sv[3] + mv[3]);
+      const half8_t lo = join(value(code_lo(k, w0), sv[0], mv[0]), value(code_lo(k, w0 >> 8), sv[1], mv[1]),
+                              value(code_lo(k, w1), sv[2], mv[2]), value(code_lo(k, w1 >> 8), sv[3], mv[3]));
+      const half8_t hi = join(value(code_hi(k, w0), sv[0], mv[0]), value(code_hi(k, w0 >> 8), sv[1], mv[1]),
+                              value(code_hi(k, w1), sv[2], mv[2]), value(code_hi(k, w1 >> 8), sv[3], mv[3]));
       acc[2 * i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, pf, acc[2 * i], 0, 0, 0);
       acc[2 * i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, pf, acc[2 * i + 1], 0, 0, 0);
       if (F16) {

@@ -41,3 +41,29 @@ def test_append_beside_saturation(vq, kind):
     pool.append(f, f, cu, np.array([[0, 2, 1]], np.int32), [0])
     np.testing.assert_array_equal(cache.codes.cpu().numpy(), pool.codes)
     np.testing.assert_array_equal(cache.scales.cpu().numpy().view(np.uint16), pool.scales.view(np.uint16))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_over_saturated_values(vq, d, kind):
+    """Groups over the whole range have the step 4368, and 15 * 4368 is beyond
+    fp16: a value is finite because the minimum is added before it is rounded."""
+    import torch
+    rng = np.random.default_rng(d)
+    n, page = 90, 32
+    k, _ = heads(rng, n, 2, d, "fp32")
+    v = torch.from_numpy((rng.choice([-1.0, 1.0], (n, 2, d)) * rng.choice([3.0, 3e4, 7e4], (n, 2, d))).astype(np.float32))
+    v[:, :, ::32], v[:, :, 1::32] = 1e5, -1e5
+    cache = new_cache(vq, 3, page, 2, d)
+    _, cu_d = offsets([n])
+    table = np.array([[1, 0, 2]], np.int32)
+    t = torch.from_numpy(table).cuda()
+    vq.kv4_append(cache, k, v.cuda(), cu_d, t)
+    pool = host_pool(cache)
+    assert np.nanmax(pool.scales[:, 1, ..., :4].astype(np.float64)) == 4368.0
+    q, q64 = heads(rng, 1, 6, d, kind)
+    ref, lref, _, mag, vsum, smag = oa.attend_ref(q64, pool, table, [n], d ** -0.5)
+    bound = oa.prompt_bound(ref, mag, vsum, smag.T, d, n, kind, "fp16", 2.0 ** -11)
+    for weigh in (False, True):
+        out = vq.kv4_attend(q, cache, t, ints([n]), add_weights=weigh)
+        check(out, ref, bound, "out")
