@@ -18,8 +18,10 @@ raise them and ``kv4_evict`` does not lower them.
 
 Every tensor has to be on one GPU.  ``stream`` (a torch stream or a raw handle;
 default: the device's current stream) is where the work is enqueued.  What a
-call allocates itself is kept for that stream; inputs made on another stream
-are the caller's to synchronise, as for any torch operation.
+call allocates itself comes from that stream's memory, and what it returns may
+be used on the caller's current stream too, once that has waited for `stream`.
+Inputs made on another stream are the caller's to synchronise, as for any torch
+operation.
 """
 
 from __future__ import annotations
@@ -28,6 +30,8 @@ import ctypes
 from typing import Optional
 
 import torch
+
+from .streams import empty as _empty, resolve as _resolve
 
 __all__ = ["VQ_F16", "KV4Cache", "attn_prompt", "attn_prompt_weights", "kv4_append", "kv4_read", "kv4_attend",
            "kv4_attend_workspace_size", "kv4_evict", "kv4_evict_workspace_size"]
@@ -93,9 +97,8 @@ def _pkg():
 
 _FN = {}
 
-# The current stream's handle and the current device without building Python
-# objects (2 us a call); the public calls where this torch has no such names.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+# The current device without building Python objects; the public call where
+# this torch has no such name.
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
@@ -106,17 +109,9 @@ def _fn(name):
     return f
 
 
-def _call(name, dev, stream, own, *args):
-    """One library call on `stream` with `dev` current; `own`: tensors this
-    call allocated, kept from reuse until the stream is done with them."""
+def _call(name, dev, handle, *args):
+    """One library call on the stream `handle` with `dev` current."""
     fn = _FN.get(name) or _fn(name)
-    if stream is None:
-        handle = _raw_stream(dev.index)
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
-        for t in own:
-            t.record_stream(st)
     if _current_device() == dev.index:
         status = fn(*args, handle)
     else:
@@ -181,12 +176,11 @@ def _ints(t, shape, dev, name: str) -> int:
     return _array(t, shape, torch.int32, dev, name)
 
 
-def _output(out, like, dev, own):
+def _output(out, like, dev, st):
     """`out`, checked, or a new tensor of `like`'s shape and type; its address."""
     if out is not None:
         return out, _array(out, like.shape, like.dtype, dev, "out")
-    out = torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype, device=dev)
-    own.append(out)
+    out = _empty(like.shape, like.dtype, dev, st)
     return out, out.data_ptr()
 
 
@@ -229,16 +223,13 @@ def attn_prompt(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, causal:
     b = _batch(q, k, cu_q, cu_k, scale, causal)
     if v.dtype != q.dtype or v.shape != k.shape:
         raise ValueError(f"v must be {q.dtype} {tuple(k.shape)}, got {v.dtype} {tuple(v.shape)}")
-    own = []
-    out, po = _output(out, q, dev, own)
-    lse = None
-    if return_lse:
-        lse = torch.empty((b.n_q_heads, b.total_q), dtype=torch.float32, device=dev)
-        own.append(lse)
     if b.n_seqs == 0 and b.total_q:
         raise ValueError("rows without a sequence")
-    pw, wb = _workspace(workspace, _fn("attn_prompt_workspace_size")(b) if workspace is None else 0, dev, own)
-    _call("attn_prompt", dev, stream, own, b, hq_, hk, hv, po, None if lse is None else lse.data_ptr(), pw, wb)
+    handle, st = _resolve(stream, dev)
+    out, po = _output(out, q, dev, st)
+    lse = _empty((b.n_q_heads, b.total_q), torch.float32, dev, st) if return_lse else None
+    ws, pw, wb = _workspace(workspace, _fn("attn_prompt_workspace_size")(b) if workspace is None else 0, dev, st)
+    _call("attn_prompt", dev, handle, b, hq_, hk, hv, po, None if lse is None else lse.data_ptr(), pw, wb)
     return (out, lse) if return_lse else out
 
 
@@ -257,19 +248,18 @@ def attn_prompt_weights(q, k, lse, cu_q, cu_k=None, scale: Optional[float] = Non
     last = int(last)
     if last < 0:
         raise ValueError(f"last must not be negative, got {last}")
-    own = []
+    if b.n_seqs == 0 and b.total_k:
+        raise ValueError("rows without a sequence")
     shape = (b.n_kv_heads, b.total_k)
+    handle, st = _resolve(stream, dev)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
-        own.append(out)
+        out = _empty(shape, torch.float32, dev, st)
     po = _array(out, shape, torch.float32, dev, "out")
-    if b.n_seqs == 0 and b.total_k:
-        raise ValueError("rows without a sequence")
     last = min(last, 2**31 - 1)
-    pw, wb = _workspace(workspace, _fn("attn_prompt_weights_workspace_size")(b, last) if workspace is None else 0, dev, own)
-    _call("attn_prompt_weights", dev, stream, own, b, hq_, hk, pl, last, int(bool(accumulate)), po, pw, wb)
+    ws, pw, wb = _workspace(workspace, _fn("attn_prompt_weights_workspace_size")(b, last) if workspace is None else 0, dev, st)
+    _call("attn_prompt_weights", dev, handle, b, hq_, hk, pl, last, int(bool(accumulate)), po, pw, wb)
     return out
 
 
@@ -356,7 +346,7 @@ def kv4_append(cache: KV4Cache, k, v, cu, block_table, start=None, pos=None, wei
     pc = _ints(cu, (s.n_seqs + 1,), dev, "cu")
     pp = None if pos is None else _ints(pos, (s.n_seqs,), dev, "pos")
     pw = None if weights is None else _array(weights, (cache.n_kv_heads, t), torch.float32, dev, "weights")
-    _call("kv4_append", dev, stream, (), cache.desc, s, hk, hv, dtype, t, pc, pp, pw)
+    _call("kv4_append", dev, _resolve(stream, dev)[0], cache.desc, s, hk, hv, dtype, t, pc, pp, pw)
 
 
 def kv4_read(cache: KV4Cache, cu, block_table, total: int, start=None, dtype=None, stream=None):
@@ -372,8 +362,9 @@ def kv4_read(cache: KV4Cache, cu, block_table, total: int, start=None, dtype=Non
         raise ValueError(f"total must not be negative, got {total}")
     pc = _ints(cu, (s.n_seqs + 1,), dev, "cu")
     shape = (total, cache.n_kv_heads, cache.head_dim)
-    k, v = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
-    _call("kv4_read", dev, stream, (k, v), cache.desc, s, pc, total, dt, k.data_ptr(), v.data_ptr())
+    handle, st = _resolve(stream, dev)
+    k, v = _empty(shape, dtype, dev, st), _empty(shape, dtype, dev, st)
+    _call("kv4_read", dev, handle, cache.desc, s, pc, total, dt, k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -382,15 +373,15 @@ def kv4_attend_workspace_size(cache: KV4Cache, n_seqs: int, n_q_heads: int, max_
     return _fn("kv4_attend_workspace_size")(cache.desc, n_seqs, n_q_heads, max_len, int(bool(add_weights)))
 
 
-def _workspace(workspace, need: int, dev, own):
+def _workspace(workspace, need: int, dev, st):
+    """The workspace (to be held until the call is queued), its address and size."""
     if workspace is None:
         if not need:
-            return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        own.append(workspace)
+            return None, None, 0
+        workspace = _empty((need,), torch.uint8, dev, st, returned=False)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def kv4_attend(q, cache: KV4Cache, block_table, lens, scale: Optional[float] = None, max_len: Optional[int] = None,
@@ -419,16 +410,13 @@ def kv4_attend(q, cache: KV4Cache, block_table, lens, scale: Optional[float] = N
     if max_len < 0:
         raise ValueError(f"max_len must not be negative, got {max_len}")
     max_len = min(max_len, capacity)
-    own = []
-    out, po = _output(out, q, dev, own)
-    lse = None
-    if return_lse:
-        lse = torch.empty((n, hq), dtype=torch.float32, device=dev)
-        own.append(lse)
+    handle, st = _resolve(stream, dev)
+    out, po = _output(out, q, dev, st)
+    lse = _empty((n, hq), torch.float32, dev, st) if return_lse else None
     weigh = int(bool(add_weights))
-    pw, wb = _workspace(workspace, kv4_attend_workspace_size(cache, n, hq, max_len, weigh) if workspace is None else 0, dev,
-                        own)
-    _call("kv4_attend", dev, stream, own, cache.desc, s, hq_, dtype, hq, d ** -0.5 if scale is None else float(scale),
+    ws, pw, wb = _workspace(workspace, kv4_attend_workspace_size(cache, n, hq, max_len, weigh) if workspace is None else 0,
+                            dev, st)
+    _call("kv4_attend", dev, handle, cache.desc, s, hq_, dtype, hq, d ** -0.5 if scale is None else float(scale),
           max_len, weigh, po, None if lse is None else lse.data_ptr(), pw, wb)
     return (out, lse) if return_lse else out
 
@@ -458,7 +446,7 @@ def kv4_evict(cache: KV4Cache, block_table, lens, next_pos, keep: int, recent: i
         raise ValueError(f"max_len must not be negative, got {max_len}")
     max_len = min(max_len, capacity)
     pn = _ints(next_pos, (s.n_seqs,), dev, "next_pos")
-    own = []
-    pw, wb = _workspace(workspace, kv4_evict_workspace_size(cache, s.n_seqs, keep, max_len) if workspace is None else 0, dev,
-                        own)
-    _call("kv4_evict", dev, stream, own, cache.desc, s, pn, min(keep, 2**31 - 1), min(recent, 2**31 - 1), max_len, pw, wb)
+    handle, st = _resolve(stream, dev)
+    ws, pw, wb = _workspace(workspace, kv4_evict_workspace_size(cache, s.n_seqs, keep, max_len) if workspace is None else 0,
+                            dev, st)
+    _call("kv4_evict", dev, handle, cache.desc, s, pn, min(keep, 2**31 - 1), min(recent, 2**31 - 1), max_len, pw, wb)
