@@ -150,11 +150,11 @@ def vq_version() -> int:
     return lib().vq_version()
 
 
-def _stream_handle(stream) -> Optional[int]:
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _stream(stream, dev):
+    """The raw handle to launch on, and the torch stream whose memory the call
+    allocates from (None: the current one)."""
+    from .streams import resolve
+    return resolve(stream, dev)
 
 
 def _as_device(a, device, dtype=None):
@@ -367,10 +367,15 @@ def _tokens(x, k: int, name: str = "x"):
     return x
 
 
-def _out(y, shape, device, name: str = "y"):
+def _new(shape, dtype, device, st, returned: bool = True):
+    from .streams import empty
+    return empty(shape, dtype, device, st, returned)
+
+
+def _out(y, shape, device, st, name: str = "y"):
     import torch
     if y is None:
-        return torch.empty(shape, dtype=torch.float32, device=device)
+        return _new(shape, torch.float32, device, st)
     _on_gpu(y, device, name)
     if y.dtype != torch.float32 or tuple(y.shape) != tuple(shape):
         raise ValueError(f"{name} must be float32 of shape {tuple(shape)}, got {y.dtype} {tuple(y.shape)}")
@@ -388,10 +393,11 @@ def vq_unpack_dequant(w: VQWeight, want_idx: bool = True, want_w: bool = True, s
     """Returns (idx [S, N, K/8] int32-viewable uint16 as torch.int16, w fp16 [N, K])."""
     import torch
     dev = _weight_device(w)
-    idx = torch.empty((w.n_stages, w.n_out, w.k_in // 8), dtype=torch.int16, device=dev) if want_idx else None
-    wt = torch.empty((w.n_out, w.k_in), dtype=torch.float16, device=dev) if want_w else None
+    handle, st = _stream(stream, dev)
+    idx = _new((w.n_stages, w.n_out, w.k_in // 8), torch.int16, dev, st) if want_idx else None
+    wt = _new((w.n_out, w.k_in), torch.float16, dev, st) if want_w else None
     _check(lib().vq_unpack_dequant(w.ref(), idx.data_ptr() if idx is not None else None,
-                                   wt.data_ptr() if wt is not None else None, _stream_handle(stream)),
+                                   wt.data_ptr() if wt is not None else None, handle),
            "vq_unpack_dequant")
     return idx, wt
 
@@ -405,8 +411,9 @@ def vq_gemv(w: VQWeight, x, y=None, stream=None):
     b = x.shape[0]
     if not 1 <= b <= 16:
         raise ValueError(f"vq_gemv takes 1..16 tokens, got {b} (use vq_gemm)")
-    y = _out(y, (b, w.n_out), dev)
-    _check(lib().vq_gemv(w.ref(), x.data_ptr(), xt, b, y.data_ptr(), _stream_handle(stream)), "vq_gemv")
+    handle, st = _stream(stream, dev)
+    y = _out(y, (b, w.n_out), dev, st)
+    _check(lib().vq_gemv(w.ref(), x.data_ptr(), xt, b, y.data_ptr(), handle), "vq_gemv")
     return y
 
 
@@ -418,7 +425,8 @@ def vq_gemm_workspace_size(w: VQWeight, m: int) -> int:
 def vq_gemm(w: VQWeight, x, y=None, workspace=None, stream=None):
     """x: bfloat16 [M, K] on the device -> y float32 [M, N].  `workspace`: a
     uint8 device tensor of at least vq_gemm_workspace_size(w, M) bytes; None
-    allocates one from torch's caching allocator when the call needs any."""
+    allocates one from torch's caching allocator when the call needs any, in
+    memory of the stream the call runs on."""
     import torch
     dev = _weight_device(w)
     x = _tokens(x, w.k_in)
@@ -426,16 +434,16 @@ def vq_gemm(w: VQWeight, x, y=None, workspace=None, stream=None):
         raise TypeError("vq_gemm takes bfloat16 activations")
     _on_gpu(x, dev, "x")
     m = x.shape[0]
-    y = _out(y, (m, w.n_out), dev)
+    handle, st = _stream(stream, dev)
+    y = _out(y, (m, w.n_out), dev, st)
     need = vq_gemm_workspace_size(w, m)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        workspace = _new((need,), torch.uint8, dev, st, returned=False) if need else None
     if workspace is not None:
         _on_gpu(workspace, dev, "workspace")
     ws_ptr = workspace.data_ptr() if workspace is not None and workspace.numel() else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().vq_gemm(w.ref(), x.data_ptr(), m, y.data_ptr(), ws_ptr, ws_bytes, _stream_handle(stream)),
-           "vq_gemm")
+    _check(lib().vq_gemm(w.ref(), x.data_ptr(), m, y.data_ptr(), ws_ptr, ws_bytes, handle), "vq_gemm")
     return y
 
 
@@ -453,8 +461,9 @@ def vq_gemm_noalloc(w: VQWeight, x, y, stream=None):
     m = x.shape[0]
     if y is None:
         raise ValueError("vq_gemm_noalloc allocates nothing: pass y")
-    y = _out(y, (m, w.n_out), dev)
-    _check(lib().vq_gemm_noalloc(w.ref(), x.data_ptr(), m, y.data_ptr(), _stream_handle(stream)), "vq_gemm_noalloc")
+    handle, st = _stream(stream, dev)
+    y = _out(y, (m, w.n_out), dev, st)
+    _check(lib().vq_gemm_noalloc(w.ref(), x.data_ptr(), m, y.data_ptr(), handle), "vq_gemm_noalloc")
     return y
 
 
@@ -469,9 +478,9 @@ def rht_apply(x, signs, max_block: int, out=None, stream=None):
     _on_gpu(x, dev, "x")
     b, n = x.shape
     _signs(signs, n, dev)
-    out = _out(out, (b, n), dev, "out")
-    _check(lib().rht_apply(x.data_ptr(), xt, b, n, signs.data_ptr(), max_block, out.data_ptr(),
-                           _stream_handle(stream)), "rht_apply")
+    handle, st = _stream(stream, dev)
+    out = _out(out, (b, n), dev, st, "out")
+    _check(lib().rht_apply(x.data_ptr(), xt, b, n, signs.data_ptr(), max_block, out.data_ptr(), handle), "rht_apply")
     return out
 
 
@@ -492,11 +501,12 @@ def rht_apply_shards(x, signs, max_block: int, shard_lens, inverse: bool = False
     if not 1 <= len(lens) <= VQ_RHT_MAX_SHARDS or min(lens) < 1 or sum(lens) != n:
         raise ValueError(f"shard lengths {lens} must be 1..{VQ_RHT_MAX_SHARDS} positive lengths summing to {n}")
     _signs(signs, n, dev)
-    out = _out(out, (b, n), dev, "out")
+    handle, st = _stream(stream, dev)
+    out = _out(out, (b, n), dev, st, "out")
     arr = (ctypes.c_int32 * len(lens))(*lens)
     _check(lib().rht_apply_shards(x.data_ptr(), xt, b, n, len(lens), ctypes.cast(arr, ctypes.c_void_p),
                                   signs.data_ptr(), max_block, 1 if inverse else 0, out.data_ptr(),
-                                  _stream_handle(stream)), "rht_apply_shards")
+                                  handle), "rht_apply_shards")
     return out
 
 
@@ -513,7 +523,8 @@ def vq_gemv_rht(w: VQWeight, x, signs, max_block: int, y=None, stream=None):
     if not 1 <= b <= 16:
         raise ValueError(f"vq_gemv_rht takes 1..16 tokens, got {b}")
     _signs(signs, w.k_in, dev)
-    y = _out(y, (b, w.n_out), dev)
-    _check(lib().vq_gemv_rht(w.ref(), x.data_ptr(), xt, b, signs.data_ptr(), max_block, y.data_ptr(),
-                             _stream_handle(stream)), "vq_gemv_rht")
+    handle, st = _stream(stream, dev)
+    y = _out(y, (b, w.n_out), dev, st)
+    _check(lib().vq_gemv_rht(w.ref(), x.data_ptr(), xt, b, signs.data_ptr(), max_block, y.data_ptr(), handle),
+           "vq_gemv_rht")
     return y

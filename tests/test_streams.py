@@ -101,3 +101,41 @@ def test_attention_allocates_on_its_stream(world, name, stream):
     for t in returned:
         recorded = [s for s in getattr(t, "recorded", []) if s != want]
         assert recorded == ([] if want == CURRENT else [CURRENT])
+
+
+def product_calls():
+    w = vq.VQWeight.__new__(vq.VQWeight)
+    w.n_out, w.k_in, w.n_stages, w.device, w.desc = 16, 64, 1, torch.device("cuda", 0), vq.VQWeightDesc()
+    x, signs = on_gpu(3, 64), on_gpu(64, dtype=torch.int8)
+    return {
+        "vq_unpack_dequant": lambda s: vq.vq_unpack_dequant(w, stream=s),
+        "vq_gemv": lambda s: vq.vq_gemv(w, x, stream=s),
+        "vq_gemm": lambda s: vq.vq_gemm(w, x, stream=s),
+        "vq_gemm_noalloc": lambda s: vq.vq_gemm_noalloc(w, x, on_gpu(3, 16, dtype=torch.float32), stream=s),
+        "rht_apply": lambda s: vq.rht_apply(x, signs, 64, stream=s),
+        "rht_apply_shards": lambda s: vq.rht_apply_shards(x, signs, 64, [32, 32], stream=s),
+        "vq_gemv_rht": lambda s: vq.vq_gemv_rht(w, x, signs, 64, stream=s),
+    }
+
+
+PRODUCTS = {"vq_unpack_dequant": 2, "vq_gemv": 1, "vq_gemm": 2, "vq_gemm_noalloc": 0, "rht_apply": 1,
+            "rht_apply_shards": 1, "vq_gemv_rht": 1}
+
+
+@pytest.mark.parametrize("name", list(PRODUCTS))
+@pytest.mark.parametrize("stream", [None, SIDE, CURRENT])
+def test_products_allocate_on_their_stream(world, monkeypatch, name, stream):
+    class Library:
+        def __getattr__(self, f):
+            return (lambda *a: 64) if f.endswith("_size") else (lambda *a: world.launched.append(a[-1]) or 0)
+
+    monkeypatch.setattr(vq, "lib", Library)
+    world.made.clear()
+    got = product_calls()[name](stream)
+    want = CURRENT if stream is None else stream
+    returned = [] if PRODUCTS[name] == 0 else list(got) if isinstance(got, tuple) else [got]
+    assert world.launched == [want] and len(world.made) == PRODUCTS[name]
+    assert [t.made_under for t in world.made] == [want] * PRODUCTS[name]
+    for t in returned:
+        recorded = [s for s in getattr(t, "recorded", []) if s != want]
+        assert recorded == ([] if want == CURRENT else [CURRENT])

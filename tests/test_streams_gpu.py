@@ -83,3 +83,29 @@ def test_default_stream_by_its_handle(vq):
         assert pool_of(got) == torch.cuda.default_stream().cuda_stream
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+def test_products_on_a_stream(vq):
+    """The same for the products and transforms."""
+    import torch
+    import vqsynth
+    from vqtest import device_weight
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        w = device_weight(vqsynth.random_weight(256, 512, 2, 12, 64, seed=3))
+        x = torch.randn((100, 512), device="cuda").bfloat16()
+        signs = (torch.randint(0, 2, (512,), device="cuda") * 2 - 1).to(torch.int8)
+    side.synchronize()
+
+    def run(stream):
+        return [*vq.vq_unpack_dequant(w, stream=stream), vq.vq_gemv(w, x[:4], stream=stream), vq.vq_gemm(w, x, stream=stream),
+                vq.rht_apply(x, signs, 512, stream=stream), vq.rht_apply_shards(x, signs, 256, [256, 256], stream=stream)]
+
+    with torch.cuda.stream(side):
+        want = run(None)
+    side.synchronize()
+    for stream in (side, side.cuda_stream):
+        got = run(stream)
+        assert [pool_of(t) for t in got] == [side.cuda_stream] * len(got)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
