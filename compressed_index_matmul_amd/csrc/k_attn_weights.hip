@@ -145,11 +145,15 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const flo
   }
 }
 
-// Pieces of the queries meet, in order.
-__global__ __launch_bounds__(kThreads) void k_attn_weights_join(const float *__restrict__ part, int64_t n, int pieces,
+// Pieces of the queries meet, in order.  Keys before the first sequence or past
+// the last have no pieces and keep what they hold, as they do without pieces.
+__global__ __launch_bounds__(kThreads) void k_attn_weights_join(const float *__restrict__ part, int64_t n, int tk, int nseq,
+                                                                const int32_t *__restrict__ cu_k, int pieces,
                                                                 int accumulate, float *__restrict__ weights) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= n) return;
+  const int key = (int)(i % tk);
+  if (key < cu_k[0] || key >= cu_k[nseq]) return;
   float sum = 0.0f;
 #pragma unroll 8
   for (int p = 0; p < pieces; ++p) sum += part[p * n + i];
@@ -169,7 +173,8 @@ hipError_t weights_d(const AttnView &a, const PromptPlan &p, const float *lse, i
   else k_attn_weights<D, BQ, F16, false><<<grid, kThreads, 0, s>>>(a, lse, last, add, to, p.pieces);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.pieces == 1) return e;
-  k_attn_weights_join<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(ws, n, p.pieces, accumulate, weights);
+  k_attn_weights_join<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(ws, n, a.tk, a.nseq, a.cu_k, p.pieces,
+                                                                                      accumulate, weights);
   return hipGetLastError();
 }
 
