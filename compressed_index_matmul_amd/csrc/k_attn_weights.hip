@@ -23,8 +23,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kKeys = 128;
-// From this |lse| on, the log2 domain's own rounding (2^-24 of it) would be
-// felt next to that of lse itself, and be many powers of two in the end.
+// Beyond this |lse| exp(s - lse) cannot be taken as exp2(s c - lse log2 e): the two
+// roundings, 2^-24 of their size, are then many powers of two.
 constexpr float kLargeLse = 1048576.0f;
 
 template <int D, int BQ, bool F16, bool CAUSAL>
@@ -33,7 +33,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const flo
   constexpr int NK = D / 16, NQ = BQ / 32;
   __shared__ __attribute__((aligned(1024))) uint16_t s_q[2][BQ * D];
   __shared__ __attribute__((aligned(16))) float s_lse[2][BQ];
-  __shared__ int s_large[2];  // some lse of the tile is beyond kLargeLse: s_lse holds them as they are
+  __shared__ __attribute__((aligned(16))) float s_raw[2][BQ];  // the lse as they came, for tiles with one beyond kLargeLse
+  __shared__ int s_large[2];
 
   const int kvh = blockIdx.x % a.hkv;
   const int piece = blockIdx.x / a.hkv % pieces, vt = blockIdx.x / a.hkv / pieces;
@@ -79,10 +80,10 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const flo
   };
   auto publish = [&](int it) {
     // rows past the end, and rows of nothing but -inf, give exp2(-inf) = 0
-    if (threadIdx.x < 64) {
-      const bool in = threadIdx.x < BQ;
-      const bool large = __any(in && fabsf(next_lse) > kLargeLse && next_lse != -INFINITY);
-      if (in) s_lse[it & 1][threadIdx.x] = next_lse == -INFINITY ? INFINITY : large ? next_lse : next_lse * kLog2e;
+    if (threadIdx.x < BQ) {
+      s_lse[it & 1][threadIdx.x] = next_lse == -INFINITY ? INFINITY : next_lse * kLog2e;
+      const bool large = __any(fabsf(next_lse) > kLargeLse && next_lse != -INFINITY);
+      if (large) s_raw[it & 1][threadIdx.x] = next_lse == -INFINITY ? INFINITY : next_lse;
       if (threadIdx.x == 0) s_large[it & 1] = large;
     }
     wait_loads();
@@ -97,8 +98,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const flo
     if (it + 1 < it1) fetch(it + 1);
     const int r0 = low + it % ni * BQ;
     const uint32_t qs = qa + (it & 1) * (BQ * D * 2);
-    const bool large = __builtin_amdgcn_readfirstlane(s_large[it & 1]) != 0;
-    const float ls = large ? a.scale : cs;
+    const int large = s_large[it & 1];
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -106,25 +106,29 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(AttnView a, const flo
       if (rw >= rq.n || (CAUSAL && rw + 31 + off < kw)) continue;  // none of these queries sees a key of the wave
       const bool mask = rw + 32 > rq.n || (CAUSAL && rw + off < kw + 31);
       float16_t S;
+      auto scores = [&] {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) S[r] = 0.0f;
+        for (int r = 0; r < 16; ++r) S[r] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NK; ++i) S = mfma32<F16>(lds_read((qs ^ (i & 7) * 32) + n * 64 * D + (i >> 3) * 256), kf[i], S);
+        for (int i = 0; i < NK; ++i) S = mfma32<F16>(lds_read((qs ^ (i & 7) * 32) + n * 64 * D + (i >> 3) * 256), kf[i], S);
+      };
+      scores();
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const float4_t l4 = *reinterpret_cast<const float4_t *>(&s_lse[it & 1][32 * n + 8 * x + 4 * h]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[4 * x + i] = __builtin_fmaf(S[4 * x + i], ls, -l4[i]);
+        for (int i = 0; i < 4; ++i) S[4 * x + i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * x + i], cs, -l4[i]));
       }
-      if (large) {
-        asm volatile("");  // a branch, as below
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[r] *= kLog2e;
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) S[r] = __builtin_amdgcn_exp2f(S[r]);
-      if (mask) {
+      if (mask | __builtin_amdgcn_readfirstlane(large)) {
         asm volatile("");  // a branch, not selects in every tile
+        if (large) {  // anew, the difference first: the common tiles pay nothing for these
+          scores();
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float l = s_raw[it & 1][32 * n + 8 * (r / 4) + 4 * h + (r & 3)];
+            S[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[r], a.scale, -l) * kLog2e);
+          }
+        }
         const int from = max(CAUSAL ? ki - off : 0, 0) - rw - 4 * h, to = rq.n - rw - 4 * h;  // the queries that count
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
