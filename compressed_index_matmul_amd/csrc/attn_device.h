@@ -123,12 +123,11 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
 }
 
-// 16 bytes a lane from base + off to LDS at `lds` + 16 lane (m0; nothing else here
-// uses it).  Not waited for:
-// wait_loads() before the barrier that publishes the tile.
+// 16 bytes a lane from base + off to LDS at `lds` + 16 lane (in m0).  Not waited
+// for: wait_loads() before the barrier that publishes the tile.
 __device__ __forceinline__ void load_to_lds(uint32_t lds, const char *base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
