@@ -36,16 +36,34 @@ from typing import Optional, Sequence
 
 import numpy as np
 
-from .attention import *  # noqa: F401,F403
-from .attention import ATTN_EXPORTS, declare as _declare_attention
-from .attention import __all__ as _attention_all
+from .attention_abi import ATTN_EXPORTS, VQ_F16, declare as _declare_attention
+
+# Looked up in .attention on first use: like the functions below it needs
+# torch, which importing the package does not.
+_ATTENTION = ("KV4Cache", "attn_prompt", "attn_prompt_weights", "kv4_append", "kv4_read", "kv4_attend",
+              "kv4_attend_workspace_size", "kv4_evict", "kv4_evict_workspace_size")
 
 __all__ = [
     "VQError", "VQWeight", "lib", "LIB_PATH", "vq_version", "vq_validate", "vq_compressed_bytes",
     "vq_unpack_dequant", "vq_gemv", "vq_gemm", "vq_gemm_workspace_size", "vq_gemm_noalloc", "rht_apply",
-    "rht_apply_shards", "vq_gemv_rht", "VQ_F32", "VQ_BF16", "VQ_STAGE_SCALES", "VQ_RHT_MAX_SHARDS", "EXPORTS",
-    *_attention_all,
+    "rht_apply_shards", "vq_gemv_rht", "VQ_F32", "VQ_BF16", "VQ_F16", "VQ_STAGE_SCALES", "VQ_RHT_MAX_SHARDS", "EXPORTS",
+    *_ATTENTION,
 ]
+
+
+def __getattr__(name):
+    if name in _ATTENTION or name in ("attention", "streams"):
+        import importlib
+        module = importlib.import_module("." + (name if name not in _ATTENTION else "attention"), __name__)
+        value = module if name not in _ATTENTION else getattr(module, name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *__all__})
+
 
 # VQMM_LIBRARY names another build of the same library (the host-sanitized
 # one the CPU tests load); by default the in-tree libvqmm.so.
