@@ -146,6 +146,8 @@ def _batch(q, k, cu_q, cu_k, scale, causal):
     if hkv < 1 or hq < 1 or hq % hkv:
         raise ValueError(f"{hq} query heads are no multiple of {hkv} key/value heads")
     dev = q.device
+    if not isinstance(cu_q, torch.Tensor):
+        raise TypeError("cu_q must be a torch tensor")
     if cu_q.dim() != 1 or cu_q.numel() < 1:
         raise ValueError("cu_q must be [sequences + 1]")
     n = cu_q.numel() - 1
@@ -241,6 +243,8 @@ class KV4Cache:
         return self
 
     def _set(self, codes, scales, weights, pos):
+        if not all(isinstance(t, torch.Tensor) for t in (codes, scales, weights, pos)):
+            raise TypeError("codes, scales, weights and pos must be torch tensors")
         if weights.dim() != 3 or scales.dim() != 6:
             raise ValueError("weights must be [pages, heads, slots] and scales [pages, 2, heads, slots / 4, groups, 8]")
         n, h, ps = weights.shape
@@ -330,6 +334,8 @@ def _workspace(workspace, need: int, dev, st):
         if not need:
             return None, None, 0
         workspace = _empty((need,), torch.uint8, dev, st, returned=False)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch tensor")
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()

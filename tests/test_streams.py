@@ -139,3 +139,13 @@ def test_products_allocate_on_their_stream(world, monkeypatch, name, stream):
     for t in returned:
         recorded = [s for s in getattr(t, "recorded", []) if s != want]
         assert recorded == ([] if want == CURRENT else [CURRENT])
+
+
+def test_arguments_that_are_no_tensors(world):
+    q, k = on_gpu(3, 4, 64), on_gpu(3, 2, 64)
+    for call in (lambda: vq.attn_prompt(q, k, k, [0, 3]), lambda: vq.attn_prompt_weights(q, k, on_gpu(4, 3), [0, 3]),
+                 lambda: vq.attn_prompt(q, k, k, on_gpu(2, dtype=torch.int32), [0, 3]),
+                 lambda: vq.attn_prompt(q, k, k, on_gpu(2, dtype=torch.int32), workspace=64),
+                 lambda: vq.KV4Cache.from_buffers([1], [2], [3], [4])):
+        with pytest.raises(TypeError):
+            call()
