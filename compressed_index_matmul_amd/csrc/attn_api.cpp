@@ -58,8 +58,8 @@ int check_batch(const attn_batch *b, AttnView *a, bool pointers = true) {
   return VQ_OK;
 }
 
-// Workgroups of one tile of `rows` queries (or keys) per sequence and head.
-bool grid_fits(int64_t total, int64_t nseq, int rows, int64_t heads) { return (total / rows + nseq) * heads <= kMaxInt; }
+// One workgroup a tile of 128 queries (or keys) of each sequence and head.
+bool grid_fits(int64_t total, int64_t nseq, int64_t heads) { return (total / 128 + nseq) * heads <= kMaxBlocks; }
 
 int check_cache(const kv4_cache *c, KvView *v, bool pointers) {
   if (!c) return VQ_ERR_NULL;
@@ -101,24 +101,24 @@ int check_rows(const KvView &v, int32_t total, const int32_t *cu) {
   if (misaligned(cu, 4)) return VQ_ERR_ALIGN;
   // four slots and eight channels a thread, 256 threads a workgroup
   const int64_t per = ((int64_t)2 * v.hkv * (v.d / 8) + 255) / 256;
-  if (((int64_t)total / 4 + 2 * (int64_t)v.nseq) * per > kMaxInt) return VQ_ERR_SHAPE;
+  if (((int64_t)total / 4 + 2 * (int64_t)v.nseq) * per > kMaxBlocks) return VQ_ERR_SHAPE;
   return VQ_OK;
 }
 
 // The sizes kv4_attend accepts (everything but pointers).
-int check_attend_sizes(const KvView &v, int n_q_heads, int max_len) {
+int check_attend_sizes(const KvView &v, int n_q_heads, int max_len, bool weigh) {
   if (n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % v.hkv != 0 || max_len < 0) return VQ_ERR_SHAPE;
   const int64_t group = n_q_heads / v.hkv;
   const int64_t rows = v.hkv * ((group + 15) / 16);  // of a sequence
-  if (((int64_t)max_len / 1024 + 1) * v.nseq * v.hkv + (int64_t)v.nseq * n_q_heads > kMaxInt) return VQ_ERR_SHAPE;
+  const int64_t chunks = weigh ? ((int64_t)max_len + 1023) / 1024 : 0;  // of the join's part for the weights
+  if (chunks * v.nseq * v.hkv + (int64_t)v.nseq * n_q_heads > kMaxBlocks) return VQ_ERR_SHAPE;
   if (v.nseq * rows > ((int64_t)1 << 22) || ((int64_t)max_len / 32 + 1) * rows > kMaxInt) return VQ_ERR_SHAPE;
   return VQ_OK;
 }
 
 int check_evict_sizes(const KvView &v, int keep, int recent, int max_len) {
   if (keep < 1 || max_len < 0) return VQ_ERR_SHAPE;
-  const int64_t rows = (int64_t)v.nseq * v.hkv, moves = std::max(0, std::min(keep, max_len - keep));
-  if (rows > ((int64_t)1 << 22) || rows * (moves / 16 + 1) > kMaxInt) return VQ_ERR_SHAPE;
+  if ((int64_t)v.nseq * v.hkv >= ((int64_t)1 << 22)) return VQ_ERR_SHAPE;  // workgroups of up to 1024 threads
   if (recent < 0 || recent > keep) return VQ_ERR_VALUE;
   return VQ_OK;
 }
@@ -140,7 +140,7 @@ int attn_prompt(const attn_batch *b, const attn_heads *q, const attn_heads *k, c
     return st;
   if ((a.tq > 0 && !out) || (ws_bytes > 0 && !workspace)) return VQ_ERR_NULL;
   if (misaligned(out, 16) || misaligned(lse, 4) || misaligned(workspace, 16)) return VQ_ERR_ALIGN;
-  if (!grid_fits(a.tq, a.nseq, 64, a.hq)) return VQ_ERR_SHAPE;
+  if (!grid_fits(a.tq, a.nseq, a.hq)) return VQ_ERR_SHAPE;
   const PromptPlan p = attn_prompt_plan(a);
   if (ws_bytes < p.bytes) return VQ_ERR_WORKSPACE;
   a.q = static_cast<const uint16_t *>(q->data);
@@ -155,7 +155,7 @@ int attn_prompt(const attn_batch *b, const attn_heads *q, const attn_heads *k, c
 
 size_t attn_prompt_workspace_size(const attn_batch *b) {
   AttnView a;
-  if (check_batch(b, &a, false) != VQ_OK || !grid_fits(a.tq, a.nseq, 64, a.hq)) return 0;
+  if (check_batch(b, &a, false) != VQ_OK || !grid_fits(a.tq, a.nseq, a.hq)) return 0;
   return attn_prompt_plan(a).bytes;
 }
 
@@ -169,7 +169,7 @@ int attn_prompt_weights(const attn_batch *b, const attn_heads *q, const attn_hea
   if (misaligned(lse, 4) || misaligned(weights, 4) || misaligned(workspace, 16)) return VQ_ERR_ALIGN;
   if (last < 0) return VQ_ERR_SHAPE;
   if (accumulate != 0 && accumulate != 1) return VQ_ERR_VALUE;
-  if (!grid_fits(a.tk, a.nseq, 64, a.hkv)) return VQ_ERR_SHAPE;
+  if (!grid_fits(a.tk, a.nseq, a.hkv)) return VQ_ERR_SHAPE;
   const PromptPlan p = attn_weights_plan(a, last);
   if (ws_bytes < p.bytes) return VQ_ERR_WORKSPACE;
   a.q = static_cast<const uint16_t *>(q->data);
@@ -182,7 +182,7 @@ int attn_prompt_weights(const attn_batch *b, const attn_heads *q, const attn_hea
 
 size_t attn_prompt_weights_workspace_size(const attn_batch *b, int32_t last) {
   AttnView a;
-  if (check_batch(b, &a, false) != VQ_OK || last < 0 || !grid_fits(a.tk, a.nseq, 64, a.hkv)) return 0;
+  if (check_batch(b, &a, false) != VQ_OK || last < 0 || !grid_fits(a.tk, a.nseq, a.hkv)) return 0;
   return attn_weights_plan(a, last).bytes;
 }
 
@@ -219,7 +219,7 @@ size_t kv4_attend_workspace_size(const kv4_cache *c, int32_t n_seqs, int32_t n_q
   if (check_cache(c, &w, false) != VQ_OK || n_seqs < 1) return 0;
   w.nseq = n_seqs;
   w.mp = (int)(kMaxInt / w.ps);
-  if (check_attend_sizes(w, n_q_heads, max_len) != VQ_OK) return 0;
+  if (check_attend_sizes(w, n_q_heads, max_len, add_weights != 0) != VQ_OK) return 0;
   return kv4_attend_plan(w, n_q_heads, max_len, add_weights != 0).bytes;
 }
 
@@ -230,7 +230,7 @@ int kv4_attend(const kv4_cache *c, const kv4_seqs *s, const attn_heads *q, int32
   int st = check_cache(c, &w, true);
   if (st != VQ_OK || (st = check_seqs(s, &w, true)) != VQ_OK) return st;
   if (dtype != VQ_BF16 && dtype != VQ_F16) return VQ_ERR_DTYPE;
-  if ((st = check_attend_sizes(w, n_q_heads, max_len)) != VQ_OK) return st;
+  if ((st = check_attend_sizes(w, n_q_heads, max_len, add_weights != 0)) != VQ_OK) return st;
   if ((st = check_heads(q, w.nseq)) != VQ_OK) return st;
   if (!std::isfinite(scale) || scale <= 0.0f || (add_weights != 0 && add_weights != 1)) return VQ_ERR_VALUE;
   if (w.nseq == 0) return VQ_OK;

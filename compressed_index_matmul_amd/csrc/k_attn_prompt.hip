@@ -394,9 +394,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnView a, PromptOut o,
 template <int D, int BN, bool F16>
 hipError_t prompt_d(const AttnView &a, const PromptPlan &p, const PromptOut &o, hipStream_t s) {
   const int tiles = a.tq / kRows + a.nseq;
-  const int64_t blocks = (int64_t)tiles * a.hq * p.pieces;
-  if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
-  const unsigned grid = (unsigned)blocks;
+  const unsigned grid = (unsigned)((int64_t)tiles * a.hq * p.pieces);
   if (p.pieces == 1) {
     if (a.causal) k_attn_prompt<D, BN, F16, true, false><<<grid, kThreads, 0, s>>>(a, o, tiles, 1);
     else k_attn_prompt<D, BN, F16, false, false><<<grid, kThreads, 0, s>>>(a, o, tiles, 1);

@@ -167,9 +167,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights_join(const float *__r
 template <int D, int BQ, bool F16>
 hipError_t weights_d(const AttnView &a, const PromptPlan &p, const float *lse, int last, bool accumulate, float *weights,
                      float *ws, hipStream_t s) {
-  const int64_t blocks = (int64_t)(a.tk / kKeys + a.nseq) * a.hkv * p.pieces;
-  if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
-  const unsigned grid = (unsigned)blocks;
+  const unsigned grid = (unsigned)((int64_t)(a.tk / kKeys + a.nseq) * a.hkv * p.pieces);
   const int64_t n = (int64_t)a.hkv * a.tk;
   float *to = p.pieces > 1 ? ws : weights;
   const int add = p.pieces == 1 && accumulate;
@@ -196,7 +194,7 @@ PromptPlan attn_weights_plan(const AttnView &a, int last) {
   const int64_t most = ((last > 0 ? std::min(last, a.tq) : a.tq) + 63) / 64 * group;
   const int64_t run = ((last > 0 ? std::min<int64_t>(last, mean) : mean) + 63) / 64 * group;
   const int64_t want = std::max<int64_t>(blocks > 0 && blocks < 384 ? 1536 / blocks : 1, (run + 63) / 64);
-  p.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 32}));
+  p.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 32, blocks > 0 ? kMaxBlocks / blocks : 1}));
   if (p.pieces > 1) p.bytes = (size_t)p.pieces * a.hkv * a.tk * 4;
   return p;
 }

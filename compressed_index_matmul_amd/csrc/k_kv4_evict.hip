@@ -311,10 +311,10 @@ template <int D>
 __global__ __launch_bounds__(kMoveThreads) void k_kv4_move(KvView c, EvictPlan p, const int32_t *__restrict__ moves,
                                                            const int32_t *__restrict__ counts, int chunks) {
   const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
-  const int i = chunk * kMovesPerBlock + threadIdx.x / kMoveLanes;
-  if (i >= counts[row]) return;
+  const int n = counts[row];
   const int32_t *to = moves + (int64_t)row * 2 * p.max_moves, *from = to + p.max_moves;
-  move_slot<D>(c, row / c.hkv, row % c.hkv, from[i], to[i], threadIdx.x % kMoveLanes);
+  for (int i = chunk * kMovesPerBlock + threadIdx.x / kMoveLanes; i < n; i += chunks * kMovesPerBlock)
+    move_slot<D>(c, row / c.hkv, row % c.hkv, from[i], to[i], threadIdx.x % kMoveLanes);
 }
 
 template <int NT, int R, int FUSE>
@@ -339,7 +339,7 @@ hipError_t evict_d(const KvView &c, const EvictPlan &p, const int32_t *next_pos,
                  : p.len_cap <= 32768 ? select_rows<1024, 32, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
                                       : select_rows<1024, 0, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s);
   if (e != hipSuccess) return e;
-  const int chunks = (p.max_moves + kMovesPerBlock - 1) / kMovesPerBlock;
+  const int chunks = (int)std::min<int64_t>((p.max_moves + kMovesPerBlock - 1) / kMovesPerBlock, kMaxBlocks / rows);
   k_kv4_move<D><<<(unsigned)(rows * chunks), kMoveThreads, 0, s>>>(c, p, moves, counts, chunks);
   return hipGetLastError();
 }

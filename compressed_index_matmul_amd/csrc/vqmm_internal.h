@@ -91,6 +91,9 @@ hipError_t launch_lowrank_gemm(const WView &w, const uint16_t *x, int m, float *
 
 // ---- attention (attn_api.cpp, k_attn_*.hip, k_kv4_*.hip) ----
 
+// Workgroups of 256 threads that one launch takes: a grid has below 2^32 work items.
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;
+
 // A validated attn_batch with its tensors.
 struct AttnView {
   int hq, hkv, d, nseq, tq, tk;

@@ -67,3 +67,30 @@ def test_attend_over_saturated_values(vq, d, kind):
     for weigh in (False, True):
         out = vq.kv4_attend(q, cache, t, ints([n]), add_weights=weigh)
         check(out, ref, bound, "out")
+
+
+def test_evict_moves_in_rounds(vq):
+    """More rows and moves than one launch has workgroups for: each takes its
+    moves in rounds.  One sequence is cut, among hundreds of empty ones; the
+    pool equals that of the sequence cut alone."""
+    import torch
+    hkv, page, keep, n, others = 32, 1024, 16400, 32700, 544
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    pages = 32
+    codes = torch.randint(0, 256, (pages, 2, hkv, page * 32), dtype=torch.uint8, device="cuda", generator=gen)
+    scales = torch.rand((pages, 2, hkv, page // 4, 2, 8), device="cuda", generator=gen).half()
+    weights = torch.rand((pages, hkv, page), device="cuda", generator=gen)
+    weights[16:] += 1.0  # nearly all that stay lie above keep
+    pos = torch.randint(0, 1000, (pages, hkv, page), dtype=torch.int32, device="cuda", generator=gen)
+    both = []
+    for seqs in (1, others):
+        cache = vq.KV4Cache.from_buffers(codes.clone(), scales.clone(), weights.clone(), pos.clone())
+        table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(seqs, 1)
+        lens = torch.zeros(seqs, dtype=torch.int32, device="cuda")
+        lens[-1] = n
+        vq.kv4_evict(cache, table, lens, torch.full_like(lens, 5000), keep=keep, recent=0, max_len=32768)
+        both.append(cache)
+    one, many = both
+    assert not torch.equal(one.pos, pos)
+    assert torch.equal(one.codes, many.codes) and torch.equal(one.scales, many.scales)
+    assert torch.equal(one.weights, many.weights) and torch.equal(one.pos, many.pos)
