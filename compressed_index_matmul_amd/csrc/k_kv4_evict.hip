@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kMoveThreads = 256;
 constexpr int kMovesPerBlock = kMoveThreads / 16;
+constexpr int kRegisterSlots = 32768;  // rows of more keep their keys in the workspace
 constexpr int kFuseMoves = 16;  // one for each 16 lanes of the smallest selecting workgroup
 
 // Keys in the order of the weights: NaN lowest, the protected slots on top.
@@ -336,7 +337,7 @@ hipError_t evict_d(const KvView &c, const EvictPlan &p, const int32_t *next_pos,
   }
   hipError_t e = p.len_cap <= 2048    ? select_rows<256, 8, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
                  : p.len_cap <= 16384 ? select_rows<1024, 16, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
-                 : p.len_cap <= 32768 ? select_rows<1024, 32, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
+                 : p.len_cap <= kRegisterSlots ? select_rows<1024, 32, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s)
                                       : select_rows<1024, 0, 0>(c, p, next_pos, keep, recent, keys, moves, counts, s);
   if (e != hipSuccess) return e;
   const int chunks = (int)std::min<int64_t>((p.max_moves + kMovesPerBlock - 1) / kMovesPerBlock, kMaxBlocks / rows);
@@ -353,7 +354,7 @@ EvictPlan kv4_evict_plan(const KvView &c, int keep, int max_len) {
   const size_t rows = (size_t)c.nseq * c.hkv;
   auto round = [](size_t x) { return (x + 255) & ~(size_t)255; };
   p.key_off = 0;
-  p.move_off = round(rows * p.len_cap * 4);
+  p.move_off = p.len_cap > kRegisterSlots ? round(rows * p.len_cap * 4) : 0;
   p.count_off = p.move_off + round(rows * 2 * p.max_moves * 4);
   p.bytes = p.max_moves > 0 ? p.count_off + round(rows * 4) : 0;
   return p;

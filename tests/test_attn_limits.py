@@ -62,3 +62,13 @@ def test_evict(L):
     assert evict(512, 1 << 16, 1 << 17) == HIP  # moves are taken in as many rounds as it needs
     assert evict((1 << 17) - 1, 16, 64) == HIP and evict(1 << 17, 16, 64) == SHAPE
     assert L.kv4_evict(c, seqs(), FAKE, 64, 0, 64, None, 0, None) == OK
+
+
+def test_evict_workspace_holds_what_is_used():
+    """Rows of up to 32768 slots keep their keys in registers."""
+    ensure_built()
+    size = vq.lib().kv4_evict_workspace_size
+    for n, keep, max_len in ((64, 1024, 32768), (64, 1024, 32769), (3, 5000, 8191), (1, 1, 2)):
+        r, moves = n * 2, min(keep, max_len - keep)
+        most = r * (8 * moves + 4 + (4 * max_len if max_len > 32768 else 0))
+        assert most <= size(cache(), n, keep, max_len) <= most + 3 * 256
