@@ -188,12 +188,18 @@ struct AttendArgs {
   float *part;    // [share][2][16][D]: a share's part of the row it begins in, and of the one it ends in
   float *stat;    // [share][2][16][2]: reference (log2 domain), sum
   float *whole;   // [seq][head][2]: the same of rows that one share covers (add_weights)
-  float *score;   // [seq][head][pitch], log2 domain (add_weights)
+  float *score;   // of each sequence after the other [head][its tiles][32], log2 domain (add_weights)
   int64_t *begins;  // [seq + 1]: tiles of one row before each sequence
 };
 
 __device__ __forceinline__ int tiles_of(const KvView &c, const AttendPlan &p, int b) {
   return (min(max(c.lens[b], 0), p.len_cap) + kTile - 1) / kTile;
+}
+
+// Where a sequence's scores begin, `before` tiles of one head after the first's.  Sequences that share pages, which
+// weights must not be added to, can pass the end: their scores fall on others', not outside.
+__device__ __forceinline__ float *scores_of(const AttendPlan &p, const AttendArgs &a, int64_t before, int tiles) {
+  return a.score + min(before, p.score_tiles - tiles) * (kTile * (int64_t)a.hq);
 }
 
 __device__ __forceinline__ int64_t uniform(int64_t v) {
@@ -208,7 +214,7 @@ struct Line {
   // the 64 sequences that the search has come to: the first of them, where it
   // begins, and of the lane's sequence the tiles and their sum up to it
   int b0;
-  int64_t base;
+  int64_t base, tiles;  // (tiles: of one row)
   uint32_t n, upto;
 };
 // Inclusive sum over the lanes of the wave.
@@ -256,22 +262,25 @@ __device__ __forceinline__ Line line_of(const KvView &c, const AttendPlan &p, in
   l.total = sum * l.rows;
   l.share = share_of<D, WEIGH>(l.total);
   l.b0 = 0;
-  l.base = 0;
+  l.base = l.tiles = 0;
   return l;
 }
 // The sequence that holds position pos < total, no earlier than the last one
-// found; where it begins and its tiles.
+// found; where it begins, the tiles of one row before it and its own.
 __device__ __forceinline__ int line_find(const KvView &c, const AttendPlan &p, Line &l, int64_t pos, int64_t *begin,
-                                         int *tiles) {
+                                         int64_t *before, int *tiles) {
   for (;;) {
     const uint64_t past = __ballot(l.base + (int64_t)l.upto * l.rows > pos);
     if (past || l.b0 + 64 >= c.nseq) {
       const int at = past ? __builtin_ctzll(past) : 63;
       *tiles = (int)lane_value(l.n, at);
-      *begin = l.base + (int64_t)(lane_value(l.upto, at) - lane_value(l.n, at)) * l.rows;
+      const uint32_t in = lane_value(l.upto, at) - lane_value(l.n, at);
+      *begin = l.base + (int64_t)in * l.rows;
+      *before = l.tiles + in;
       return min(l.b0 + at, c.nseq - 1);
     }
     l.base += (int64_t)lane_value(l.upto, 63) * l.rows;
+    l.tiles += lane_value(l.upto, 63);
     l.b0 += 64;
     l.n = tiles64(c, p, l.b0);
     l.upto = prefix64(l.n);
@@ -304,6 +313,7 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
   asm volatile("" : "+v"(tid));  // anew for each row: what follows from it would else be kept in registers throughout
   const int lane = tid & 63, col = lane & 15, h4 = lane >> 4;
   int b, row, t_begin, t_end, ntiles;
+  int64_t before = 0;
   if (LONE) {
     row = blockIdx.x % (c.hkv * p.htiles);
     b = blockIdx.x / (c.hkv * p.htiles);
@@ -313,7 +323,7 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
     pos = pos_end;
   } else {
     int64_t begin;
-    b = __builtin_amdgcn_readfirstlane(line_find(c, p, line, pos, &begin, &ntiles));
+    b = __builtin_amdgcn_readfirstlane(line_find(c, p, line, pos, &begin, &before, &ntiles));
     const int in = (int)(pos - begin);  // a sequence's tiles over all rows are below 2^31
     row = __builtin_amdgcn_readfirstlane(in / ntiles);
     t_begin = __builtin_amdgcn_readfirstlane(in - row * ntiles);
@@ -376,6 +386,9 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
   float mref = -INFINITY, lsum = 0.0f;
   bool large = false;  // some head's reference is beyond kLargeRef
 
+  float *scores = nullptr;  // of the lane's head and slots, from the sequence's first tile on
+  if (WEIGH) scores = scores_of(p, a, before, ntiles) + (int64_t)(head0 + col) * ntiles * kTile + 4 * h4;
+
   const int tpp = c.ps / kTile;  // tiles of a page
   const int64_t code_head = (int64_t)c.ps * (D / 2), scale_head = (int64_t)c.ps * (DG * 2);
   // Keys and values of the next tile go into the registers of this one as soon
@@ -422,7 +435,7 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
       }
     }
     if (WEIGH && col < heads) {
-      float *sp = a.score + ((int64_t)b * a.hq + head0 + col) * p.score_pitch + tile * kTile + 4 * h4;
+      float *sp = scores + (int64_t)tile * kTile;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         *reinterpret_cast<float4_t *>(sp + 16 * u) = float4_t{S[u][0] * cs, S[u][1] * cs, S[u][2] * cs, S[u][3] * cs};
@@ -648,11 +661,14 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
   const int len = min(max(c.lens[b], 0), p.len_cap);
   if (chunk * kWeighSlots >= len) return;
   const int slot = chunk * kWeighSlots + threadIdx.x * 4;
+  const int nt = (int)(a.begins[b + 1] - a.begins[b]);
+  const float *scores = scores_of(p, a, a.begins[b], nt) + slot;
   float4_t w = {0.0f, 0.0f, 0.0f, 0.0f};
   const int wave = threadIdx.x >> 6;
   for (int ht = 0; ht < p.htiles; ++ht) {  // heads of the group, 16 at a time
     const int ng = min(16, p.group - ht * 16);
-    const int64_t at0 = (int64_t)b * a.hq + kvh * p.group + ht * 16;
+    const int head0 = kvh * p.group + ht * 16;
+    const int64_t at0 = (int64_t)b * a.hq + head0;
     const Parts parts = parts_of(a, total, share, rows, b, kvh * p.htiles + ht);
     __syncthreads();
     for (int g = wave; g < ng; g += kWaves) {
@@ -664,7 +680,7 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
     if (slot < len)
 #pragma unroll 8
       for (int g = 0; g < ng; ++g) {
-        const float4_t x = *reinterpret_cast<const float4_t *>(a.score + (at0 + g) * p.score_pitch + slot);
+        const float4_t x = *reinterpret_cast<const float4_t *>(scores + (int64_t)(head0 + g) * nt * kTile);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(x[i] - s_top[g]), s_inv[g], w[i]);
       }
@@ -712,17 +728,20 @@ AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add
   p.group = n_q_heads / c.hkv;
   p.htiles = (p.group + 15) / 16;
   p.len_cap = (int)std::min<int64_t>(max_len, (int64_t)c.mp * c.ps);
+  // weights go to pages of one sequence each, so all sequences together hold no more than the pool
+  const int64_t pool = (int64_t)c.np * c.ps;
+  if (add_weights) p.len_cap = (int)std::min<int64_t>(p.len_cap, pool);
   const int64_t rows = (int64_t)c.nseq * c.hkv * p.htiles;
   p.lone = !add_weights && p.len_cap <= kLoneSlots && rows <= 256;
   if (p.lone) return p;
-  p.score_pitch = (p.len_cap + kTile - 1) / kTile * kTile;
+  p.score_tiles = std::min((int64_t)c.nseq * ((p.len_cap + kTile - 1) / kTile), pool / kTile);
   auto round = [](size_t x) { return (x + 255) & ~(size_t)255; };
   const size_t pieces = (size_t)shares_of(c.d) * 2 * 16, heads = (size_t)c.nseq * n_q_heads;
   p.stat_off = round(pieces * c.d * 4);
   p.begin_off = p.stat_off + round(pieces * 8);
   p.whole_off = p.begin_off + round(((size_t)c.nseq + 1) * 8);
   p.score_off = p.whole_off + (add_weights ? round(heads * 8) : 0);
-  p.bytes = p.score_off + (add_weights ? round(heads * p.score_pitch * 4) : 0);
+  p.bytes = p.score_off + (add_weights ? round((size_t)p.score_tiles * kTile * n_q_heads * 4) : 0);
   return p;
 }
 

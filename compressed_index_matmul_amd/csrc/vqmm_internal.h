@@ -138,7 +138,7 @@ struct AttendPlan {
   int htiles;       // 16-head tiles of a group
   bool lone;        // short and few rows: one workgroup of more waves takes each whole
   int len_cap;      // lengths are clamped to this
-  int score_pitch;  // floats per head of stored scores (add_weights)
+  int64_t score_tiles;  // tiles of every head's stored scores (add_weights)
   size_t stat_off, begin_off, whole_off, score_off, bytes;
 };
 AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add_weights);

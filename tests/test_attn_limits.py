@@ -72,3 +72,16 @@ def test_evict_workspace_holds_what_is_used():
         r, moves = n * 2, min(keep, max_len - keep)
         most = r * (8 * moves + 4 + (4 * max_len if max_len > 32768 else 0))
         assert most <= size(cache(), n, keep, max_len) <= most + 3 * 256
+
+
+def test_attend_workspace_grows_with_the_pool():
+    """Scores are kept for slots that the pool can hold, not for every
+    sequence at its bound."""
+    ensure_built()
+    size = vq.lib().kv4_attend_workspace_size
+    c = cache(n_pages=200, page_size=64, n_kv_heads=8, head_dim=128)
+    plain = size(c, 64, 64, 131072, 0)
+    scores = size(c, 64, 64, 131072, 1) - plain
+    assert 200 * 64 * 64 * 4 <= scores <= 200 * 64 * 64 * 4 + 64 * 64 * 8 + 512
+    # and no more than the bound where that is less
+    assert size(c, 2, 64, 100, 1) - plain <= 2 * 128 * 64 * 4 + 2 * 64 * 8 + 512

@@ -94,3 +94,43 @@ def test_evict_moves_in_rounds(vq):
     assert not torch.equal(one.pos, pos)
     assert torch.equal(one.codes, many.codes) and torch.equal(one.scales, many.scales)
     assert torch.equal(one.weights, many.weights) and torch.equal(one.pos, many.pos)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 3, 1), (128, 40, 2), (256, 4, 2)])
+def test_weights_with_a_wide_table(vq, d, hq, hkv):
+    """Weights added over a table far wider than the pool: the workspace is the
+    pool's, results and weights are those of a table that just fits; more than
+    64 sequences, empty ones among them."""
+    import torch
+    rng = np.random.default_rng(d)
+    page = 32
+    lens = [int(n) for n in rng.integers(0, 70, 90)]
+    lens[3], lens[60], lens[70], lens[89] = 0, 1200, 0, 333
+    used = [-(-n // page) for n in lens]
+    order = rng.permutation(sum(used))
+    table = np.zeros((90, 4000), np.int32)
+    at = 0
+    for b, n in enumerate(used):
+        table[b, :n] = order[at:at + n]
+        at += n
+    _, cu_d = offsets(lens)
+    k, _ = heads(rng, sum(lens), hkv, d, "bf16")
+    v, _ = heads(rng, sum(lens), hkv, d, "bf16")
+    q, _ = heads(rng, 90, hq, d, "bf16")
+    cache = new_cache(vq, sum(used), page, hkv, d)
+    wide = torch.from_numpy(table).cuda()
+    narrow = wide[:, :max(used)].contiguous()
+    vq.kv4_append(cache, k, v, cu_d, narrow)
+    results = []
+    for t in (narrow, wide):
+        cache.weights.zero_()
+        need = vq.kv4_attend_workspace_size(cache, 90, hq, t.shape[1] * page, True)
+        assert need < vq.kv4_attend_workspace_size(cache, 90, hq, 2000, False) + sum(used) * page * hq * 4 + 90 * hq * 8 + 1024
+        ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+        out, lse = vq.kv4_attend(q, cache, t, ints(lens), add_weights=True, return_lse=True, workspace=ws)
+        results.append((out, lse, cache.weights.clone()))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    # every head of a sequence that is not empty hands out a weight of one
+    total = results[0][2].double().sum().item()
+    np.testing.assert_allclose(total, hq * sum(n > 0 for n in lens), rtol=1e-5)
