@@ -110,7 +110,8 @@ int check_attend_sizes(const KvView &v, int n_q_heads, int max_len, bool weigh) 
   if (n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % v.hkv != 0 || max_len < 0) return VQ_ERR_SHAPE;
   const int64_t group = n_q_heads / v.hkv;
   const int64_t rows = v.hkv * ((group + 15) / 16);  // of a sequence
-  const int64_t chunks = weigh ? ((int64_t)max_len + 1023) / 1024 : 0;  // of the join's part for the weights
+  // of the join's part for the weights, whose lengths are bounded by the pool too
+  const int64_t chunks = weigh ? (std::min<int64_t>(max_len, (int64_t)v.np * v.ps) + 1023) / 1024 : 0;
   if (chunks * v.nseq * v.hkv + (int64_t)v.nseq * n_q_heads > kMaxBlocks) return VQ_ERR_SHAPE;
   if (v.nseq * rows > ((int64_t)1 << 22) || ((int64_t)max_len / 32 + 1) * rows > kMaxInt) return VQ_ERR_SHAPE;
   return VQ_OK;

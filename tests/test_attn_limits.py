@@ -42,7 +42,7 @@ def test_cache_calls(L):
 
 
 def test_attend(L):
-    c = cache(n_kv_heads=8, head_dim=128)
+    c = cache(n_pages=1 << 16, n_kv_heads=8, head_dim=128)
     s = seqs(n_seqs=4096, max_pages=1 << 18)
 
     def attend(max_len, weigh):
@@ -51,6 +51,8 @@ def test_attend(L):
     assert attend(1 << 20, 0) == HIP  # only the join of added weights grows with the lengths
     assert attend(1 << 20, 1) == SHAPE and L.kv4_attend_workspace_size(c, 4096, 32, 1 << 20, 1) == 0
     assert attend(500 * 1024, 1) == HIP
+    c.n_pages = 1 << 10
+    assert attend(1 << 20, 1) == HIP  # and no further than the pool
 
 
 def test_evict(L):
