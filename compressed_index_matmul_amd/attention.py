@@ -287,7 +287,8 @@ def kv4_append(cache: KV4Cache, k, v, cu, block_table, start=None, pos=None, wei
     cu int32 [sequences + 1], block_table int32 [sequences, pages], start
     int32 [sequences]; pos int32 [sequences], the position of each sequence's
     first row (None: its slot); weights float32 [Hkv, T], the slots' accumulated
-    weight so far (None: 0).  The caller raises the lengths."""
+    weight so far (None: 0).  The caller raises the lengths.  A page that is
+    written to must belong to one sequence of the table."""
     s = _seqs(cache, block_table, start, "start")
     dev = cache.device
     hk, hv = _heads(k, "k", dev), _heads(v, "v", dev)
@@ -349,7 +350,8 @@ def kv4_attend(q, cache: KV4Cache, block_table, lens, scale: Optional[float] = N
     max_len: the host's bound on lens (longer ones count as max_len; default:
     the block table's capacity); a close one saves launch width and workspace.
     add_weights adds every slot's attention weight, summed over the heads of
-    its group, to cache.weights.  workspace: a device tensor of at least
+    its group, to cache.weights; the pages must then not be shared between
+    sequences (otherwise they may).  workspace: a device tensor of at least
     kv4_attend_workspace_size bytes (None allocates).  Returns out, with
     return_lse also float32 [sequences, Hq].  An empty sequence gives zeros
     and -inf."""
@@ -388,7 +390,8 @@ def kv4_evict(cache: KV4Cache, block_table, lens, next_pos, keep: int, recent: i
     """Cut every sequence longer than `keep` down to keep slots, each key/value
     head on its own: kept are the slots with pos >= next_pos[b] - recent, then
     those of the largest cache.weights.  Kept slots at or above keep move into
-    the free ones below.  lens and next_pos (the position of the next token)
+    the free ones below: every page of a sequence that is cut must belong to it
+    alone (copy a shared prefix first).  lens and next_pos (the position of the next token)
     are int32 [sequences]; the caller then lowers lens to min(lens, keep)."""
     s = _seqs(cache, block_table, lens, "lens")
     if lens is None:

@@ -435,8 +435,8 @@ typedef struct attn_batch {
  *   lse : float [n_q_heads][total_q], or NULL
  * A query that sees no key gives out = 0 and lse = -inf.  Scores, the running
  * maximum and sum and the output sum are fp32; the probabilities enter the
- * second product rounded to the 16-bit type of v (relative error 2^-9 for
- * VQ_BF16; for VQ_F16 2^-12 down to 2^-21 of the row's largest, an absolute
+ * second product rounded to the 16-bit type of v (relative error 2^-8 for
+ * VQ_BF16; for VQ_F16 2^-11 down to 2^-21 of the row's largest, an absolute
  * 2^-32 of it below), which leaves a 16-bit result 1.0 to 1.4 times the error
  * of its last rounding alone.  Key rows outside a sequence never reach its
  * result, whatever they hold.
@@ -516,7 +516,10 @@ typedef struct kv4_seqs {
  * Store packed keys and values: row cu[b] + i goes to slot lens[b] + i of
  * sequence b (lens: the length before the call, which the caller then raises;
  * NULL means 0), for each key/value head.  Rows past the block table's
- * capacity are dropped.
+ * capacity are dropped.  A page that a call writes to has to belong to one
+ * sequence of the table: of rows for the same slot any one may end up there.
+ * (Sequences may share the pages of a common prefix as long as it is only
+ * read.)
  *   k, v    : [total][n_kv_heads][head_dim] of `dtype`, VQ_F32, VQ_BF16 or
  *             VQ_F16 (VQ_F32 is what the compressed products give)
  *   cu      : int32 [n_seqs + 1] on the device
@@ -542,13 +545,16 @@ int kv4_read(const kv4_cache *c, const kv4_seqs *s, const int32_t *cu, int32_t t
  * the 4-bit cache:
  *   q       : [n_seqs][n_q_heads][head_dim] of dtype, VQ_BF16 or VQ_F16
  *   max_len : the host's bound on lens; a longer length counts as max_len
- *             (and every length as at most max_pages * page_size)
+ *             (and every length as at most max_pages * page_size, where
+ *             weights are added as at most the pool)
  *   add_weights : 1 adds each slot's weight, summed over the heads of its
  *             group, to the cache's weights (pages shared between sequences
  *             must not be added to); 0 leaves them
  *   out     : [n_seqs][n_q_heads][head_dim] of dtype
  *   lse     : float [n_seqs][n_q_heads], or NULL
- *   workspace : 16-byte aligned, at least kv4_attend_workspace_size bytes
+ *   workspace : 16-byte aligned, at least kv4_attend_workspace_size bytes.
+ *             Adding weights keeps a float of every slot and query head there:
+ *             as many as max_len allows, or the pool where that is less
  * An empty sequence gives out = 0, lse = -inf.  Scores are exact sums of
  * 16-bit queries and integer codes, scaled and summed in fp32 (queries are
  * held in fp16 after a power-of-two rescale per head, exact for every value
@@ -574,6 +580,10 @@ size_t kv4_attend_workspace_size(const kv4_cache *c, int32_t n_seqs, int32_t n_q
  * free ones below it, the lowest to the lowest, with their weight and
  * position; everything else stays where it is.  The caller then lowers the
  * lengths to min(lens, keep).  Attention does not depend on the slots' order.
+ * Slots are moved within the sequence's own pages, so every page of a sequence
+ * that is cut has to belong to it alone: a prefix that sequences share has to
+ * be copied for each of them first, or the others find other tokens in it, and
+ * moves of two sequences in one call race.
  *   next_pos : int32 [n_seqs], the position of the next token
  *   keep     : >= 1;  recent : 0..keep
  *   max_len  : as for kv4_attend
