@@ -134,3 +134,73 @@ def test_weights_with_a_wide_table(vq, d, hq, hkv):
     # every head of a sequence that is not empty hands out a weight of one
     total = results[0][2].double().sum().item()
     np.testing.assert_allclose(total, hq * sum(n > 0 for n in lens), rtol=1e-5)
+
+
+def attend_case(vq, kind, hq, hkv, d, page, lens, seed):
+    """Results against the oracle, with and without weights."""
+    import torch
+    rng = np.random.default_rng(seed)
+    per = -(-max(lens) // page)
+    table = rng.permutation(len(lens) * per).reshape(len(lens), per).astype(np.int32)
+    cache = new_cache(vq, table.size, page, hkv, d)
+    _, cu_d = offsets(lens)
+    k, _ = heads(rng, sum(lens), hkv, d, "fp32", 1.0, 1.5)
+    v, _ = heads(rng, sum(lens), hkv, d, "fp32")
+    t = torch.from_numpy(table).cuda()
+    vq.kv4_append(cache, k, v, cu_d, t)
+    q, q64 = heads(rng, len(lens), hq, d, kind)
+    ref, lref, _, mag, vsum, smag = oa.attend_ref(q64, host_pool(cache), table, lens, d ** -0.5)
+    bound = oa.prompt_bound(ref, mag, vsum, smag.T, d, max(lens), kind, "fp16", 2.0 ** -11)
+    for weigh in (False, True):
+        out, lse = vq.kv4_attend(q, cache, t, ints(lens), add_weights=weigh, return_lse=True)
+        check(out, ref, bound, f"out, weigh {weigh}")
+        check(lse, lref, oa.lse_bound(lref, smag, d, max(lens)), "lse")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (20, 1)])
+def test_attend_wide_heads_in_shares(vq, hq, hkv, kind):
+    """Heads of 256 beyond what one workgroup takes whole: rows cut over
+    several shares, short and empty ones beside them, a group of more than 16."""
+    attend_case(vq, kind, hq, hkv, 256, 96, [2500, 3, 0, 129, 1100], seed=hq)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,hkv", [(1024, 1), (1025, 1), (1024, 128), (1024, 129), (40, 129)])
+def test_attend_where_its_form_changes(vq, n, hkv, kind):
+    """Both sides of the length and the number of rows up to which a workgroup
+    takes a row whole."""
+    attend_case(vq, kind, hkv, hkv, 64, 32, [n, 7], seed=n + hkv)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[60, 60], [1500, 60]])
+def test_attend_query_that_is_not_finite(vq, lens, d, bad):
+    """It reaches its own head and no other: sequences and key/value heads
+    beside it keep their bits, query heads of its group their results within
+    the bound (they share its reference maximum's updates)."""
+    import torch
+    rng = np.random.default_rng(d)
+    page, per = 64, -(-max(lens) // 64)
+    table = rng.permutation(2 * per).reshape(2, per).astype(np.int32)
+    cache = new_cache(vq, table.size, page, 2, d)
+    _, cu_d = offsets(lens)
+    k, _ = heads(rng, sum(lens), 2, d, "bf16")
+    v, _ = heads(rng, sum(lens), 2, d, "bf16")
+    t = torch.from_numpy(table).cuda()
+    vq.kv4_append(cache, k, v, cu_d, t)
+    q, _ = heads(rng, 2, 4, d, "bf16")
+    want, lse = vq.kv4_attend(q, cache, t, ints(lens), return_lse=True)
+    ref, _, _, mag, vsum, smag = oa.attend_ref(q.double().cpu().numpy(), host_pool(cache), table, lens, d ** -0.5)
+    bound = oa.prompt_bound(ref, mag, vsum, smag.T, d, max(lens), "bf16", "fp16", 2.0 ** -11)
+    q[0, 1, 5] = bad
+    for weigh in (False, True):
+        got, l2 = vq.kv4_attend(q, cache, t, ints(lens), add_weights=weigh, return_lse=True)
+        assert not bool(torch.isfinite(got[0, 1]).any()) and not bool(torch.isfinite(l2[0, 1]))
+        check(got[0, :1], ref[0, :1], bound[0, :1], "the head beside it")
+        check(got[0, 2:], ref[0, 2:], bound[0, 2:], "the other key/value head")
+        check(got[1], ref[1], bound[1], "the other sequence")
+        if not weigh:
+            assert torch.equal(got[0, 2:], want[0, 2:]) and torch.equal(got[1], want[1])
+            assert torch.equal(l2[0, 2:], lse[0, 2:]) and torch.equal(l2[1], lse[1])
