@@ -43,7 +43,16 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kLoneWaves = 8;  // of a workgroup that takes a whole sequence and head
 constexpr int kTile = 32;  // slots a wave takes at a time
-constexpr int kLoneSlots = 1024;
+// Where no weights are added, a workgroup takes a row whole up to this many slots.  Measured in graphs, one workgroup a
+// row against shares and their join (us; 32/8 heads of 128, all lengths equal, then spread evenly up to the bound):
+//   rows       8               256                          2048
+//   512    6.9 /  8.5    7.5 / 15.5,  7.2 / 20.8     52 / 49,  45 / 80
+//   1024  10.2 /  8.7   12.8 / 19.6, 10.7 / 31.4    101 / 86,  62 / 98
+//   2048  16.5 /  9.0   20.8 / 26.1, 19.3 / 37.4    175 / 152, 114 / 114
+// so it wins wherever rows are many and unequal, and loses where few rows are long: at 1024 slots 1.5 us, less than the
+// 4 us that the second launch and its workspace cost a caller outside a graph.  Heads of 64 cross there too (8 rows: 7.4 /
+// 7.9, 2048 slots 11.7 / 8.0); heads of 256 earlier (512 slots 10.5 / 10.0, 768 13.4 / 10.5, 1024 16.3 / 10.5).
+constexpr int lone_slots(int d) { return d == 256 ? 768 : 1024; }
 // Workgroups of four waves that 256 CUs hold at once, by their registers.
 // Heads of 128: four workgroups a CU (128 registers, 8 bytes spilled) took 41 us where three took 45 for 32 x 4096
 // slots of 32/8 heads; with weights, whose scores are written as well, four took 143 us and three 138 for the 300,000
@@ -721,8 +730,6 @@ hipError_t attend_d(const KvView &c, const AttendPlan &p, const AttendArgs &a, b
 
 }  // namespace
 
-// One workgroup a row where rows are short and fewer than the CUs: no second
-// launch.
 AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add_weights) {
   AttendPlan p{};
   p.group = n_q_heads / c.hkv;
@@ -731,8 +738,7 @@ AttendPlan kv4_attend_plan(const KvView &c, int n_q_heads, int max_len, bool add
   // weights go to pages of one sequence each, so all sequences together hold no more than the pool
   const int64_t pool = (int64_t)c.np * c.ps;
   if (add_weights) p.len_cap = (int)std::min<int64_t>(p.len_cap, pool);
-  const int64_t rows = (int64_t)c.nseq * c.hkv * p.htiles;
-  p.lone = !add_weights && p.len_cap <= kLoneSlots && rows <= 256;
+  p.lone = !add_weights && p.len_cap <= lone_slots(c.d);
   if (p.lone) return p;
   p.score_tiles = std::min((int64_t)c.nseq * ((p.len_cap + kTile - 1) / kTile), pool / kTile);
   auto round = [](size_t x) { return (x + 255) & ~(size_t)255; };

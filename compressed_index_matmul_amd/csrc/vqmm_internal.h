@@ -136,7 +136,7 @@ hipError_t launch_kv4_read(const KvView &c, const int32_t *cu, int total, int dt
 struct AttendPlan {
   int group;        // query heads per key/value head
   int htiles;       // 16-head tiles of a group
-  bool lone;        // short and few rows: one workgroup of more waves takes each whole
+  bool lone;        // short rows: one workgroup of more waves takes each whole
   int len_cap;      // lengths are clamped to this
   int64_t score_tiles;  // tiles of every head's stored scores (add_weights)
   size_t stat_off, begin_off, whole_off, score_off, bytes;

@@ -166,11 +166,14 @@ def test_attend_wide_heads_in_shares(vq, hq, hkv, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
-@pytest.mark.parametrize("n,hkv", [(1024, 1), (1025, 1), (1024, 128), (1024, 129), (40, 129)])
-def test_attend_where_its_form_changes(vq, n, hkv, kind):
-    """Both sides of the length and the number of rows up to which a workgroup
-    takes a row whole."""
-    attend_case(vq, kind, hkv, hkv, 64, 32, [n, 7], seed=n + hkv)
+@pytest.mark.parametrize("n,hkv,d", [(1024, 1, 64), (1025, 1, 64), (1024, 129, 64), (40, 129, 64), (1024, 2, 128),
+                                     (1025, 2, 128), (768, 1, 256), (769, 1, 256)])
+def test_attend_where_its_form_changes(vq, n, hkv, d, kind):
+    """Both sides of the length up to which a workgroup takes a row whole, and
+    more rows than CUs."""
+    need = vq.kv4_attend_workspace_size(vq.KV4Cache(1, 32, hkv, d), 2, hkv, n)
+    assert (need == 0) == (n in (40, 768, 1024))
+    attend_case(vq, kind, hkv, hkv, d, 32, [n, 7], seed=n + hkv)
 
 
 @pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
