@@ -260,7 +260,6 @@ __device__ __forceinline__ Line line_of(const KvView &c, const AttendPlan &p, in
   const bool leave = blockIdx.x == 0 && threadIdx.x < 64;
   if (leave && (int)threadIdx.x < c.nseq) begins[threadIdx.x] = l.upto - l.n;
   int64_t sum = lane_value(l.upto, 63);
-#pragma unroll 4
   for (int b0 = 64; b0 < c.nseq; b0 += 64) {
     const uint32_t n = tiles64(c, p, b0), upto = prefix64(n);
     if (leave && b0 + (int)threadIdx.x < c.nseq) begins[b0 + threadIdx.x] = sum + (upto - n);
@@ -333,7 +332,10 @@ __global__ __launch_bounds__(NW *kWave, (LONE ? 2 : kSharesPerCu<D, WEIGH>)) voi
   } else {
     int64_t begin;
     b = __builtin_amdgcn_readfirstlane(line_find(c, p, line, pos, &begin, &before, &ntiles));
-    const int in = (int)(pos - begin);  // a sequence's tiles over all rows are below 2^31
+    // Lengths that another stream shortens meanwhile are found shorter here than when the line was made: the bounds
+    // keep such a row within the arrays, and the share moves on by a tile at least.
+    ntiles = max(ntiles, 1);
+    const int in = (int)min(pos - begin, (int64_t)ntiles * line.rows - 1);  // below 2^31
     row = __builtin_amdgcn_readfirstlane(in / ntiles);
     t_begin = __builtin_amdgcn_readfirstlane(in - row * ntiles);
     t_end = __builtin_amdgcn_readfirstlane((int)min((int64_t)ntiles, t_begin + (pos_end - pos)));
@@ -667,10 +669,10 @@ __global__ __launch_bounds__(kThreads) void k_kv4_join(KvView c, AttendPlan p, A
   const int chunk = id % chunks;
   id /= chunks;
   const int kvh = id % c.hkv, b = id / c.hkv;
-  const int len = min(max(c.lens[b], 0), p.len_cap);
+  const int nt = (int)(a.begins[b + 1] - a.begins[b]);
+  const int len = min(min(max(c.lens[b], 0), p.len_cap), nt * kTile);  // the scores there are
   if (chunk * kWeighSlots >= len) return;
   const int slot = chunk * kWeighSlots + threadIdx.x * 4;
-  const int nt = (int)(a.begins[b + 1] - a.begins[b]);
   const float *scores = scores_of(p, a, a.begins[b], nt) + slot;
   float4_t w = {0.0f, 0.0f, 0.0f, 0.0f};
   const int wave = threadIdx.x >> 6;
