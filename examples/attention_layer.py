@@ -51,9 +51,12 @@ class AttentionLayer:
 
     def __init__(self, n_seqs, d_model=576, hq=9, hkv=3, d=64, keep=256, recent=64, max_len=2048, page=64, seed=0):
         self.hq, self.hkv, self.d, self.keep, self.recent = hq, hkv, d, keep, recent
+        pages = -(-max_len // page)
+        self.capacity = pages * page
+        if not 1 <= keep < self.capacity:  # a token is stored before the budget is enforced
+            raise ValueError(f"keep={keep} leaves no free slot in a cache of {self.capacity} slots a sequence")
         self.wqkv = synthetic_weight((hq + 2 * hkv) * d, d_model, seed)
         self.wo = synthetic_weight(d_model, hq * d, seed + 1)
-        pages = -(-max_len // page)
         self.cache = vq.KV4Cache(n_seqs * pages, page, hkv, d)
         dev = self.cache.device
         self.table = torch.arange(n_seqs * pages, dtype=torch.int32, device=dev).view(n_seqs, pages)
@@ -80,12 +83,15 @@ class AttentionLayer:
 
     def prompt(self, x, lengths):
         """x bfloat16 [sum(lengths), d_model]: the packed prompts."""
+        if max(lengths) > self.capacity:
+            raise ValueError(f"a prompt of {max(lengths)} tokens in a cache of {self.capacity} slots a sequence")
         dev = x.device
         cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device=dev)
         pos = torch.cat([torch.arange(n, device=dev) for n in lengths])
         q, k, v = self._qkv(x, pos)
-        out, lse = vq.attn_prompt(q, k.to(x.dtype), v.to(x.dtype), cu, return_lse=True)
-        got = vq.attn_prompt_weights(q, k.to(x.dtype), lse, cu)
+        kh = k.to(x.dtype)
+        out, lse = vq.attn_prompt(q, kh, v.to(x.dtype), cu, return_lse=True)
+        got = vq.attn_prompt_weights(q, kh, lse, cu)
         vq.kv4_append(self.cache, k.contiguous(), v, cu, self.table, weights=got)  # float32 rows, as the product gives them
         self.lens += cu[1:] - cu[:-1]
         self.next_pos += cu[1:] - cu[:-1]
