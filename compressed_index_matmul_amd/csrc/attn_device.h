@@ -70,8 +70,9 @@ __device__ __forceinline__ Rows seq_rows(const int32_t *cu, int b, int total) {
 // tile numbers from cu[b] / rows + extra * b up to those of b + 1, which are
 // at least the ceil(n / rows) (extra = 1) it needs, whatever the lengths;
 // the spare ones have nothing to do.  Returns the sequence of tile number t
-// (-1: none) and its first tile number.  cu is clamped and taken as its own
-// running maximum by the search, so any contents end the search in range.
+// (-1: none) and its first tile number.  cu is clamped to the rows and the
+// search ends in range whatever it holds; offsets that fall give wrong rows,
+// never rows outside.
 __device__ __forceinline__ int find_tile(const int32_t *cu, int nseq, int total, int rows, int extra, int t, int *first) {
   int lo = 0, hi = nseq - 1;  // the last b with start(b) <= t
   while (lo < hi) {

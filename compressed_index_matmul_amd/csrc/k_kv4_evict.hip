@@ -4,7 +4,7 @@
 // key by a radix search (four passes of 8 bits over keys that order as the
 // weights do), splits its ties by slot, and lists the free slots below keep
 // and the kept ones at or above it, both in ascending order; there are equally
-// many.  k_kv4_move copies slot to slot, a wave a move: sources lie at or above
+// many.  k_kv4_move copies slot to slot, 16 lanes a move: sources lie at or above
 // keep and targets below it, so no copy reads what another writes.  Counts are
 // integers and every list position is a prefix sum, so nothing depends on the
 // order in which waves run.
