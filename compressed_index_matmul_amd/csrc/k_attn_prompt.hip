@@ -13,7 +13,11 @@
 //                 registers; V^T comes out of row-major LDS by the transposing
 //                 reads (4 keys x 16 channels a group of 16 lanes).
 // The reference maximum may lag the running one by 2^8, so most tiles skip the
-// rescale of O.
+// rescale of O.  P takes v's 16-bit type, as the product's other operand: its
+// rounding leaves results 1.25 times the error of a 16-bit result of the fp32 form
+// (relative 2.0e-3 and 1.6e-3 in bf16).  A second product with P's remainder ends
+// that and was not taken: half as many matrix instructions again, 729 -> 967 us for
+// the prompts below.
 //
 // Bound: the matrix cores and, sharing each SIMD's issue with them, the vector
 // work of the softmax (about 100 instructions a lane for 32 keys, 16 of
@@ -24,8 +28,9 @@
 // waves took 751 us where 32 and three took 731.  Under this load the clock falls to
 // about 1.8 GHz (a library product of 8192^3 with its matrix cores 93% busy runs at
 // 1.4), so instructions saved count twice.  Measured: 14,919 tokens in five prompts,
-// 32/8 heads of 128, bf16, causal: 740 us, 1.0 PFLOP/s (a bf16 library product
-// reached 1.35 to 1.41); 4096 + 2000 tokens of 16/4 heads of 256: 195 us, 0.87 PFLOP/s.
+// 32/8 heads of 128, bf16, causal: 729 us a pass, 1.0 PFLOP/s (a bf16 library product
+// reached 1.35 to 1.41; 776 us is the median of 30 traced ones, at a lower clock);
+// 4096 + 2000 tokens of 16/4 heads of 256: 190 us, 0.90 PFLOP/s.
 #include "attn_device.h"
 
 #include <algorithm>

@@ -10,9 +10,9 @@
 //
 // Bound: vector issue (an exponential, a fused multiply-add and an add a pair)
 // next to 2 head_dim flops on the matrix cores.  Every query of 8191 + 2000
-// tokens, 32/8 heads of 128: 309 us, 0.94 PFLOP/s.  7620 keys of three prompts
-// against their last 64 queries: 12.8 us, mostly the latency of four rounds;
-// every query of 2048 + 701, 9/3 heads of 64: 11.3 + 4.0 us.
+// tokens, 32/8 heads of 128: 324 + 5 us, 0.89 PFLOP/s.  7620 keys of three prompts
+// against their last 64 queries: 13.1 us, mostly the latency of four rounds;
+// every query of 2048 + 701, 9/3 heads of 64: 11.4 + 3.9 us.
 #include "attn_device.h"
 
 #include <algorithm>

@@ -27,10 +27,11 @@
 // Bound: HBM, 2 (head_dim / 2 + head_dim / 8) bytes a slot and head; next to it
 // vector issue (330 instructions a tile of 32 slots and 128 channels: steps and
 // minima of the keys, unpacking, steps and minima of the values).  Measured:
-// four sequences of 300,000 slots in all, 64/8 heads of 128, fp16: 95 us, 4.1 TB/s
-// (102 us with the join); with weights 104 us, 4.6 TB/s with the scores it
-// writes, and 24 us for the join that reads them.  One sequence of 1001 slots
-// of 32/8 heads, one launch: 10.5 us.
+// four sequences of 300,000 slots in all, 64/8 heads of 128, fp16: 93 us, 4.1 TB/s,
+// and 6 us for the join; with weights 106 us, 4.4 TB/s with the scores it
+// writes, and 23 us for the join that reads them.  32 x 4096 slots of 32/8 heads:
+// 34 us, 4.9 TB/s, and 5; 256 sequences of 200 to 1900 slots: 94 us, 3.6 TB/s, and
+// 14.  One launch: one sequence of 1001 slots 10.5 us, 256 of up to 1000 68 us.
 #include "attn_device.h"
 
 #include <algorithm>

@@ -13,7 +13,7 @@
 // halves, never read back, so neighbouring slots keep what they hold and no
 // two threads write the same byte.  The four threads of a group exchange
 // minimum and maximum through DPP.  8192 rows of 8 heads of 128 in bf16: append
-// 13.4 us (3.3 TB/s of rows and cache), read 9.7 us (4.6 TB/s).
+// 13.6 us (3.3 TB/s of rows and cache), read 9.6 us (4.6 TB/s).
 #include "attn_device.h"
 
 namespace vqmm {
