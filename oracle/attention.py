@@ -90,13 +90,14 @@ def prompt_bound(out, mag, vsum, smag, d, n, kind, p_kind=None, v_round=0.0):
     A score is an fp32 sum of d exact products (off by d 2^-24 of their
     magnitudes), times scale log2(e) in fp32 (2^-22 of itself); exp2 and the sum of
     n terms add (n + 4) 2^-24.  Twice that, for numerator and sum, is the
-    relative error of a probability, which is then rounded to 16 bits (below
-    fp16's normal range off by 2^-25, at most 2^8 times that after the lag of
-    the reference maximum, which itself divides out: 2^-24 of each |v|); values
-    may carry v_round; the result is rounded once."""
+    relative error of a probability, which is then rounded to 16 bits.  fp16
+    ones are taken so that the largest is 2^7 at least: below fp16's normal
+    range they are off by 2^-25, 2^-32 of the largest, which is at most one, so
+    by 2^-32 of each |v|.  Values may carry v_round; the result is rounded
+    once."""
     s = np.swapaxes(smag, 0, 1)[:, :, None]
     delta = 2.0 * (s * (d + 8) * 2.0 ** -24 + s * 2.0 ** -22 + (n + 4) * 2.0 ** -24)
-    err = (delta + ROUND[p_kind or kind] + v_round) * 1.01 * mag + 2.0 ** -24 * vsum
+    err = (delta + ROUND[p_kind or kind] + v_round) * 1.01 * mag + 2.0 ** -32 * vsum
     return err + ROUND[kind] * 1.01 * (np.abs(out) + err) + 2.0 ** -25
 
 

@@ -132,11 +132,9 @@ def sinks(rng, n, d, at, below, kind):
 
 
 def thin(ref, mag, vsum, smag, largest, d, n, kind, **kw):
-    """prompt_bound for probabilities that are rounded to fp16 with room for
-    them: its 2^-24 of sum |v| allows for fp16's subnormal step of 2^-24 below
-    a largest probability of one; the largest is 2^7 at least here, so the step
-    is 2^-31 of it and its half 2^-32."""
-    return oa.prompt_bound(ref, mag, vsum * largest * 2.0 ** -8, smag, d, n, kind, **kw)
+    """prompt_bound where the largest probability of the row is known: what is
+    below fp16's normal range is off by 2^-32 of it."""
+    return oa.prompt_bound(ref, mag, vsum * largest, smag, d, n, kind, **kw)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
