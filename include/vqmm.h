@@ -437,7 +437,7 @@ typedef struct attn_batch {
  * maximum and sum and the output sum are fp32; the probabilities enter the
  * second product rounded to the 16-bit type of v (relative error 2^-8 for
  * VQ_BF16; for VQ_F16 2^-11 down to 2^-21 of the row's largest, an absolute
- * 2^-32 of it below), which leaves a 16-bit result 1.0 to 1.4 times the error
+ * 2^-32 of it below), which leaves a 16-bit result 1.2 to 1.4 times the error
  * of its last rounding alone.  Key rows outside a sequence never reach its
  * result, whatever they hold.
  *   workspace : 16-byte aligned, at least attn_prompt_workspace_size bytes
