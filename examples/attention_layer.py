@@ -73,8 +73,8 @@ class AttentionLayer:
     def _qkv(self, x, pos):
         y = self._project(self.wqkv, x).view(x.shape[0], -1, self.d)
         q, k, v = y.split([self.hq, self.hkv, self.hkv], 1)
-        q, k = vq.attn_rotate(q, k, pos, self.rotary, q_weight=self.norms[0], k_weight=self.norms[1], dtype=x.dtype)
-        return q, k, v.to(x.dtype)
+        q, k = vq.attn_rotate(q, k, pos, self.rotary, q_weight=self.norms[0], k_weight=self.norms[1])
+        return q.to(x.dtype), k, v  # the cache takes float32 rows, as the product gives them
 
     def _evict(self):
         if self.window is not None or self.max_len <= self.keep:
@@ -92,11 +92,12 @@ class AttentionLayer:
         cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device=dev)
         pos = torch.cat([torch.arange(n, dtype=torch.int32, device=dev) for n in lengths])
         q, k, v = self._qkv(x, pos)
+        kh, vh = k.to(x.dtype), v.to(x.dtype)
         if self.window is None:
-            out, lse = vq.attn_prompt(q, k, v, cu, return_lse=True)
-            got = vq.attn_prompt_weights(q, k, lse, cu)
+            out, lse = vq.attn_prompt(q, kh, vh, cu, return_lse=True)
+            got = vq.attn_prompt_weights(q, kh, lse, cu)
         else:
-            out, got = vq.attn_prompt(q, k, v, cu, window=self.window, sinks=self.sinks), None
+            out, got = vq.attn_prompt(q, kh, vh, cu, window=self.window, sinks=self.sinks), None
         vq.kv4_append(self.cache, k, v, cu, self.table, weights=got)
         self.lens += cu[1:] - cu[:-1]
         self.next_pos += cu[1:] - cu[:-1]
