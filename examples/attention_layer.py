@@ -22,7 +22,12 @@ few, and nothing is evicted:
     attn_rotate -> attn_prompt (window) -> ...       kv4_append -> kv4_attend_chunk (window) -> ...
 
 Several tokens a sequence at once (the next piece of a prompt, drafted tokens)
-go through kv4_append and kv4_attend_chunk in either case.  Needs an MI355X and the built library.
+go through kv4_append and kv4_attend_chunk in either case.  Under a budget what
+their queries looked at is counted when slots have to go:
+
+    kv4_attend_chunk (log sums) -> kv4_read -> attn_prompt_weights -> kv4_evict
+
+Needs an MI355X and the built library.
 """
 import argparse
 import os
@@ -63,6 +68,7 @@ class AttentionLayer:
         self.next_pos = torch.zeros(n_seqs, dtype=torch.int32, device=dev)  # tokens seen
         self.step_cu = torch.arange(n_seqs + 1, dtype=torch.int32, device=dev)
         self.max_len = 0  # the host's bound on lens
+        self.chunks = []  # since the last eviction: queries, their offsets, the lengths after them, bounds on both
         self.rotary = vq.Rotary(d, device=dev)
         gen = torch.Generator(device=dev).manual_seed(seed)
         self.norms = [1.0 + 0.1 * torch.randn(d, generator=gen, device=dev) for _ in range(2)] if norm else [None, None]
@@ -79,10 +85,30 @@ class AttentionLayer:
     def _evict(self):
         if self.window is not None or self.max_len <= self.keep:
             return
+        for chunk in self.chunks:
+            self._count(*chunk)
+        self.chunks.clear()
         vq.kv4_evict(self.cache, self.table, self.lens, self.next_pos, keep=self.keep, recent=self.recent,
                      max_len=self.max_len)
         self.lens.clamp_(max=self.keep)
         self.max_len = self.keep
+
+    def _count(self, q, cu, lens, max_q, max_len):
+        """Adds what a chunk's queries gave each slot to the cache's weights.  Only evictions need it, so it waits for
+        one: no slot moves before.  Keys are read back in q's 16 bits, which a ranking can bear."""
+        _, lse = vq.kv4_attend_chunk(q, self.cache, self.table, lens, cu, max_len=max_len, max_q=max_q, return_lse=True)
+        n, ps = len(lens), self.cache.page_size
+        ends = lens.cumsum(0, dtype=torch.int32)
+        rows = torch.arange(n * max_len, dtype=torch.int32, device=q.device)  # more than there are: lens is not on the host
+        cu_k = torch.cat([ends.new_zeros(1), ends])
+        k, _ = vq.kv4_read(self.cache, cu_k, self.table, len(rows), dtype=q.dtype)
+        got = torch.zeros((self.hkv, len(rows)), device=q.device)
+        vq.attn_prompt_weights(q, k, lse, cu, cu_k, out=got)  # rows of no sequence keep their zeros
+        seq = torch.searchsorted(ends, rows, right=True).clamp_(max=n - 1)
+        slot = (rows - cu_k[seq]).clamp_(max=self.capacity - 1)
+        page = self.table[seq, slot // ps].long()
+        heads = torch.arange(self.hkv, device=q.device)
+        self.cache.weights.index_put_((page[:, None], heads, (slot % ps).long()[:, None]), got.T, accumulate=True)
 
     def prompt(self, x, lengths):
         """x bfloat16 [sum(lengths), d_model]: the packed prompts."""
@@ -122,6 +148,8 @@ class AttentionLayer:
         self.max_len += max(lengths)
         out = vq.kv4_attend_chunk(q, self.cache, self.table, self.lens, cu, window=self.window, sinks=self.sinks,
                                   max_len=self.max_len, max_q=max(lengths))
+        if self.window is None:
+            self.chunks.append((q, cu, self.lens.clone(), max(lengths), self.max_len))
         self._evict()
         return self._project(self.wo, out.view(x.shape[0], -1))
 
