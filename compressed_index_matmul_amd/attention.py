@@ -183,9 +183,10 @@ def attn_prompt(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, causal:
     differently: a chunk against its prefix) int32 [sequences + 1] offsets.
     causal: query i of Lq sees keys j <= i + Lk - Lq.  A query that sees no key
     gives zeros (lse -inf).  window (with causal): of these, only the newest
-    `window` and the sequence's first `sinks`.  workspace: a device tensor (None allocates what
-    the call needs).  Returns out [Tq, Hq, D], with return_lse also the scores'
-    log sum of exponentials, float32 [Hq, Tq]."""
+    `window` and the sequence's first `sinks`.  workspace: a device tensor (None
+    allocates what the call needs; fewer rows may need more).  Returns out [Tq,
+    Hq, D], with return_lse also the scores' log sum of exponentials, float32
+    [Hq, Tq]."""
     hq_ = _heads(q, "q")
     dev = q.device
     hk, hv = _heads(k, "k", dev), _heads(v, "v", dev)
@@ -402,7 +403,8 @@ def kv4_attend(q, cache: KV4Cache, block_table, lens, scale: Optional[float] = N
 
 def kv4_attend_chunk_workspace_size(cache: KV4Cache, n_seqs: int, n_q_heads: int, total_q: int, max_len: int,
                                     max_q: Optional[int] = None, window: Optional[int] = None, sinks: int = 0) -> int:
-    """Bytes of workspace kv4_attend_chunk needs (max_q None: total_q)."""
+    """Bytes of workspace that serve kv4_attend_chunk for these sizes and for
+    smaller ones, window and sinks being the same (max_q None: total_q)."""
     return _fn("kv4_attend_chunk_workspace_size")(cache.desc, n_seqs, n_q_heads, total_q, *_window(window, sinks), max_len,
                                                   total_q if max_q is None else max_q)
 
@@ -421,9 +423,9 @@ def kv4_attend_chunk(q, cache: KV4Cache, block_table, lens, cu_q=None, scale: Op
     max_len: the host's bound on lens (longer ones count as max_len; default:
     the block table's capacity); max_q: its bound on the queries of a sequence
     (default: Tq), which chooses how the work is cut.  workspace: a device tensor
-    of at least kv4_attend_chunk_workspace_size bytes (None allocates).  Returns
-    out [Tq, Hq, D], with return_lse also float32 [Hq, Tq].  A query that sees
-    nothing gives zeros and -inf."""
+    of at least kv4_attend_chunk_workspace_size bytes, of these sizes or of the
+    largest call's (None allocates).  Returns out [Tq, Hq, D], with return_lse
+    also float32 [Hq, Tq].  A query that sees nothing gives zeros and -inf."""
     s = _seqs(cache, block_table, lens, "lens")
     if lens is None:
         raise ValueError("kv4_attend_chunk needs lens")

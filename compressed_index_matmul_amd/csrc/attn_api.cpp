@@ -332,7 +332,7 @@ size_t kv4_attend_chunk_workspace_size(const kv4_cache *c, int32_t n_seqs, int32
   if (check_cache(c, &w, false) != VQ_OK || n_seqs < 1) return 0;
   w.nseq = n_seqs;
   if (check_chunk_sizes(w, n_q_heads, total_q, window, sinks, max_len, max_q) != VQ_OK) return 0;
-  return kv4_chunk_plan(w, n_q_heads, total_q, window, sinks, max_len, max_q).bytes;
+  return kv4_chunk_bytes(w, n_q_heads, total_q, window, sinks, max_len, max_q);
 }
 
 int kv4_attend_chunk(const kv4_cache *c, const kv4_seqs *s, const attn_heads *q, int32_t dtype, int32_t n_q_heads,

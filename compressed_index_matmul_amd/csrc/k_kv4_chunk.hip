@@ -518,19 +518,33 @@ static int lone_waves(int d, int64_t slots, int64_t tiles) {
   return slots <= (tiles >= 128 ? 1280 : 512) ? 4 : 0;
 }
 
+// Row tiles of a call, at most.
+int64_t kv4_chunk_blocks(const KvView &c, int n_q_heads, int total_q) {
+  return ((int64_t)total_q * (n_q_heads / c.hkv) / kRows + c.nseq) * c.hkv;
+}
+
+// Slots that a row tile meets, at most.
+static int64_t visible_slots(const ChunkPlan &p, int max_len) {
+  return std::min<int64_t>(max_len, (int64_t)p.window + p.sinks + kRows);
+}
+
 // Whether k_kv4_chunk takes row tiles whole: where they are many, so that shares gain nothing and walk past the newest
 // slots of a chunk's first rows (4096 tokens on their own, 32/8 heads of 128: shares 268 us, whole 178; two of 3000 on 5000
 // slots 520 / 442; six of 1000 on 1900 to 6000 446 / 416), or slots few (eight chunks of 300 tokens on 800 slots: 9/3 heads
 // of 64 39 / 31, 32/8 of 128 87 / 79, 16/4 of 256 98 / 74).  Otherwise shares: 1000 tokens on 2000 slots 32 / 51, 62 / 73 and
 // 82 / 141, one of 1024 on its own 25 / 30, 45 / 43 and 67 / 80.
-static bool whole_row_tiles(int64_t slots, int64_t tiles) {
-  return tiles >= 384 || slots <= 512 || (slots <= 1024 && tiles >= 80);
+static bool whole_row_tiles(const KvView &c, const ChunkPlan &p, int total_q, int max_len) {
+  const int64_t slots = visible_slots(p, max_len), tiles = (int64_t)total_q * p.group / kRows * c.hkv;
+  return tiles >= 384 || slots <= 512 || (slots <= 1024 && tiles >= 80) ||
+         kv4_chunk_blocks(c, p.group * c.hkv, total_q) * (kRows / kJoinRows) > kMaxBlocks / 2;  // the second launch's limit
 }
 
-// Row tiles of a call, at most.
-int64_t kv4_chunk_blocks(const KvView &c, int n_q_heads, int total_q) {
-  return ((int64_t)total_q * (n_q_heads / c.hkv) / kRows + c.nseq) * c.hkv;
-}
+// The workspace's areas: sums of the parts with their references and sums of p, for either kernel, and where each sequence
+// begins.
+constexpr size_t kPlaces = (size_t)kShares * 2 * kRows;
+static size_t chunk_area(const KvView &c) { return kPlaces * (c.d * 4 + 8); }
+static size_t few_area(const KvView &c) { return kv4_few_sums(c) + kv4_few_sums(c) / c.d * 2; }
+static size_t begins_area(const KvView &c) { return (((size_t)c.nseq + 1) * 4 + 255) & ~(size_t)255; }
 
 ChunkPlan kv4_chunk_plan(const KvView &c, int n_q_heads, int total_q, int window, int sinks, int max_len, int max_q) {
   ChunkPlan p{};
@@ -540,30 +554,40 @@ ChunkPlan kv4_chunk_plan(const KvView &c, int n_q_heads, int total_q, int window
   p.sinks = std::min(sinks, max_len);
   p.page_blocks = c.ps / 32;
   p.page_mul = (uint32_t)((((uint64_t)1 << 32) + p.page_blocks - 1) / p.page_blocks);
-  const int64_t visible = std::min<int64_t>(max_len, (int64_t)p.window + p.sinks + kRows);
   const bool all_few = (int64_t)max_q * p.group <= kFewRows;
   p.any_few = (all_few || c.nseq > 1) && kv4_few_takes(c, p, total_q);
   p.any_chunk = !(p.any_few && all_few);
   p.few = !p.any_few ? 0 : all_few ? INT_MAX : kFewRows;
-  p.lone = lone_waves(c.d, visible, ((int64_t)total_q * p.group / kFewRowTile + c.nseq) * c.hkv);
-  p.whole = whole_row_tiles(visible, (int64_t)total_q * p.group / kRows * c.hkv) ||
-            kv4_chunk_blocks(c, n_q_heads, total_q) * (kRows / kJoinRows) > kMaxBlocks / 2;  // the second launch's limit
-  auto round = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  const size_t begins = round(((size_t)c.nseq + 1) * 4);
+  p.lone = lone_waves(c.d, visible_slots(p, max_len), ((int64_t)total_q * p.group / kFewRowTile + c.nseq) * c.hkv);
+  p.whole = whole_row_tiles(c, p, total_q, max_len);
   if (p.any_chunk && !p.whole) {
-    const size_t places = (size_t)kShares * 2 * kRows;
-    p.stat_off = places * c.d * 4;
-    p.begin_off = p.stat_off + places * 8;
-    p.bytes = p.begin_off + begins;
+    p.stat_off = kPlaces * c.d * 4;
+    p.begin_off = chunk_area(c);
+    p.bytes = p.begin_off + begins_area(c);
   }
   if (p.any_few && !p.lone) {
     p.join_few = p.any_chunk || (int64_t)total_q * n_q_heads > kJoinSingly;
     p.few_off = p.bytes;
     p.few_stat_off = p.few_off + kv4_few_sums(c);
-    p.few_begin_off = p.few_stat_off + kv4_few_sums(c) / c.d * 2;
-    p.bytes = p.few_begin_off + begins;
+    p.few_begin_off = p.few_off + few_area(c);
+    p.bytes = p.few_begin_off + begins_area(c);
   }
   return p;
+}
+
+// Enough for a call of these sizes and for every smaller one.  Which areas a plan has goes up and down with its sizes (row
+// tiles are taken whole where they are many, and where slots are few), what an area takes does not: so these are the areas
+// of any call with up to as many sequences, queries, slots and queries a sequence.  k_kv4_chunk has its area if it has with
+// the fewest queries that go to it, k_kv4_few if it has with one sequence.  (Only sequences beyond the second launch's
+// limit are counted as they are: theirs are whole.)
+size_t kv4_chunk_bytes(const KvView &c, int n_q_heads, int total_q, int window, int sinks, int max_len, int max_q) {
+  if (total_q == 0) return 0;
+  const ChunkPlan p = kv4_chunk_plan(c, n_q_heads, total_q, window, sinks, max_len, max_q);
+  const int fewest = std::min(total_q, kFewRows / p.group + 1);
+  size_t n = 0;
+  if (p.any_chunk && !whole_row_tiles(c, p, fewest, max_len)) n += chunk_area(c) + begins_area(c);
+  if (!lone_waves(c.d, visible_slots(p, max_len), c.hkv)) n += few_area(c) + begins_area(c);
+  return n;
 }
 
 hipError_t launch_kv4_chunk(const KvView &c, const ChunkPlan &p, const ChunkCall &x, void *ws, hipStream_t s) {

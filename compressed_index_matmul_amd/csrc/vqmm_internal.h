@@ -188,6 +188,7 @@ struct ChunkCall {
   float *lse;
 };
 ChunkPlan kv4_chunk_plan(const KvView &c, int n_q_heads, int total_q, int window, int sinks, int max_len, int max_q);
+size_t kv4_chunk_bytes(const KvView &c, int n_q_heads, int total_q, int window, int sinks, int max_len, int max_q);
 int64_t kv4_chunk_blocks(const KvView &c, int n_q_heads, int total_q);
 // The few-row kernel: bytes of its sums (their references and sums take 8 a row more), whether it takes these sizes.
 size_t kv4_few_sums(const KvView &c);

@@ -450,7 +450,8 @@ int attn_prompt(const attn_batch *b, const attn_heads *q, const attn_heads *k, c
                 float *lse, void *workspace, size_t ws_bytes, void *stream);
 
 /* Bytes of workspace attn_prompt needs; 0 for none and for sizes it refuses
- * (the pointers of b are not looked at).  Host only. */
+ * (the pointers of b are not looked at).  These are for this batch's sizes:
+ * fewer rows may be cut into more pieces and need more.  Host only. */
 size_t attn_prompt_workspace_size(const attn_batch *b);
 
 /*
@@ -463,6 +464,7 @@ size_t attn_prompt_workspace_size(const attn_batch *b);
 int attn_prompt_window(const attn_batch *b, int32_t window, int32_t sinks, const attn_heads *q, const attn_heads *k,
                        const attn_heads *v, void *out, float *lse, void *workspace, size_t ws_bytes, void *stream);
 
+/* As attn_prompt_workspace_size, for this batch's sizes.  Host only. */
 size_t attn_prompt_window_workspace_size(const attn_batch *b, int32_t window, int32_t sinks);
 
 /*
@@ -481,7 +483,8 @@ size_t attn_prompt_window_workspace_size(const attn_batch *b, int32_t window, in
 int attn_prompt_weights(const attn_batch *b, const attn_heads *q, const attn_heads *k, const float *lse, int32_t last,
                         int32_t accumulate, float *weights, void *workspace, size_t ws_bytes, void *stream);
 
-/* Bytes of workspace attn_prompt_weights needs; as above.  Host only. */
+/* Bytes of workspace attn_prompt_weights needs, for this batch's sizes; as
+ * above.  Host only. */
 size_t attn_prompt_weights_workspace_size(const attn_batch *b, int32_t last);
 
 /* ----------------------------------------------------------------------
@@ -639,6 +642,7 @@ size_t kv4_attend_workspace_size(const kv4_cache *c, int32_t n_seqs, int32_t n_q
  *   out     : [total_q][n_q_heads][head_dim] of dtype
  *   lse     : float [n_q_heads][total_q], or NULL
  *   workspace : 16-byte aligned, at least kv4_attend_chunk_workspace_size bytes
+ *             of these sizes or of larger ones
  * n_kv_heads (total_q group / 256 + n_seqs) is below 2^23, and times (max_len / 32
  * + 4) below 2^31 - 1024; total_q group is below 2^30 and n_seqs below 2^22
  * (VQ_ERR_SHAPE otherwise; group = n_q_heads / n_kv_heads).
@@ -657,7 +661,11 @@ int kv4_attend_chunk(const kv4_cache *c, const kv4_seqs *s, const attn_heads *q,
                      int32_t max_q, void *out, float *lse, void *workspace, size_t ws_bytes, void *stream);
 
 /* Bytes of workspace kv4_attend_chunk needs; 0 for none and for sizes it
- * refuses.  Host only. */
+ * refuses.  They are enough for every smaller call too: one of the same
+ * cache, n_q_heads, window and sinks with no more sequences, queries, slots
+ * (max_len) and queries a sequence (max_q).  (Sequences: as long as n_seqs
+ * n_kv_heads + n_q_heads is below 2^19; beyond, of as many.)  A call may need
+ * less.  Host only. */
 size_t kv4_attend_chunk_workspace_size(const kv4_cache *c, int32_t n_seqs, int32_t n_q_heads, int32_t total_q,
                                        int32_t window, int32_t sinks, int32_t max_len, int32_t max_q);
 
