@@ -26,7 +26,7 @@
 // split8): twice as many products, errors of 2.8e-4 of the result where its own rounding leaves 2.1e-4, and 4.9e-4 without.
 //
 // The work is cut into 256 equal shares of a line of tiles (Cut) whose parts a second launch joins, or row tiles are
-// taken whole (whole_row_tiles).  Sequences of up to 64 rows go to k_kv4_few.
+// taken whole (few_slots, many_even_tiles).  Sequences of up to 64 rows go to k_kv4_few.
 //
 // Bound: matrix cores and vector issue, which two waves a SIMD overlap in part (matrix cores busy 43 % of the cycles,
 // vector units 51 %, some wave issuing in 92 %, clock 1.95 GHz: the time behaves as the sum of the two); in calls of few
@@ -528,16 +528,31 @@ static int64_t visible_slots(const ChunkPlan &p, int max_len) {
   return std::min<int64_t>(max_len, (int64_t)p.window + p.sinks + kRows);
 }
 
-// Whether k_kv4_chunk takes row tiles whole: where they are many, so that shares gain nothing and walk past the newest
-// slots of a chunk's first rows (4096 tokens on their own, 32/8 heads of 128: shares 268 us, whole 178; two of 3000 on 5000
-// slots 520 / 442; six of 1000 on 1900 to 6000 446 / 416), or slots few (eight chunks of 300 tokens on 800 slots: 9/3 heads
-// of 64 39 / 31, 32/8 of 128 87 / 79, 16/4 of 256 98 / 74).  Otherwise shares: 1000 tokens on 2000 slots 32 / 51, 62 / 73 and
-// 82 / 141, one of 1024 on its own 25 / 30, 45 / 43 and 67 / 80.
-static bool whole_row_tiles(const KvView &c, const ChunkPlan &p, int total_q, int max_len) {
-  const int64_t slots = visible_slots(p, max_len), tiles = (int64_t)total_q * p.group / kRows * c.hkv;
-  return tiles >= 384 || slots <= 512 || (slots <= 1024 && tiles >= 80) ||
-         kv4_chunk_blocks(c, p.group * c.hkv, total_q) * (kRows / kJoinRows) > kMaxBlocks / 2;  // the second launch's limit
+// Whether k_kv4_chunk takes row tiles whole.
+// So where slots are few (eight chunks of 300 tokens on 800 slots, shares / whole: 9/3 heads of 64 39 / 31 us, 32/8 of 128
+// 87 / 79, 16/4 of 256 98 / 74; but 1000 tokens on 2000 slots 32 / 51, 62 / 73 and 82 / 141, and one chunk of 1024 on its
+// own 25 / 30, 45 / 43 and 67 / 80).
+static bool few_slots(int64_t slots, int64_t tiles) { return slots <= 512 || (slots <= 1024 && tiles >= 80); }
+// And where row tiles are many, so that shares gain nothing and walk past the newest slots of a chunk's first rows (4096
+// tokens on their own, 32/8 heads of 128: 260 / 176; two of 3000 on 5000 slots 492 / 409; six of 1000 on 1900 to 6000 414 /
+// 376), unless a single one may walk much longer than all take together: the lengths are not on the host, and one long
+// sequence beside short ones would go on alone (four of 1200 on their own and 30 tokens after 60,000: 206 / 1328; 16 of 512
+// and one of 512 on 8000: 211 / 242, heads of 256 222 / 503).  What all take at least is counted by the queries' own tokens,
+// one sequence of max_q and the others of equal length.  At five times that whole row tiles still win or tie (2000 tokens on
+// 10,000 slots beside three of 2000 on their own, heads of 128, 2.6 times: 558 / 441; heads of 256, 5.1 times: 576 / 621),
+// at seven times they lose in the unequal batches above (and a prompt of 4096 on its own whose bound says 32,000: 256 / 160).
+static bool many_even_tiles(const KvView &c, const ChunkPlan &p, int64_t slots, int64_t tiles, int total_q, int max_q) {
+  if (tiles < 384) return false;
+  auto pairs = [&](double queries) { return queries * std::min<double>(queries, p.window) / 2; };
+  const int longest = std::min(max_q, total_q), others = std::max(c.nseq - 1, 1);
+  const double own = pairs(longest) + others * pairs((double)(total_q - longest) / others);
+  return slots <= 5 * own * p.group * c.hkv / (kRows * (double)kShares);
 }
+// The second launch's limit leaves no choice.
+static bool joins_past_grid(const KvView &c, const ChunkPlan &p, int total_q) {
+  return kv4_chunk_blocks(c, p.group * c.hkv, total_q) * (kRows / kJoinRows) > kMaxBlocks / 2;
+}
+static int64_t row_tiles(const KvView &c, const ChunkPlan &p, int total_q) { return (int64_t)total_q * p.group / kRows * c.hkv; }
 
 // The workspace's areas: sums of the parts with their references and sums of p, for either kernel, and where each sequence
 // begins.
@@ -554,12 +569,13 @@ ChunkPlan kv4_chunk_plan(const KvView &c, int n_q_heads, int total_q, int window
   p.sinks = std::min(sinks, max_len);
   p.page_blocks = c.ps / 32;
   p.page_mul = (uint32_t)((((uint64_t)1 << 32) + p.page_blocks - 1) / p.page_blocks);
+  const int64_t visible = visible_slots(p, max_len), tiles = row_tiles(c, p, total_q);
   const bool all_few = (int64_t)max_q * p.group <= kFewRows;
   p.any_few = (all_few || c.nseq > 1) && kv4_few_takes(c, p, total_q);
   p.any_chunk = !(p.any_few && all_few);
   p.few = !p.any_few ? 0 : all_few ? INT_MAX : kFewRows;
-  p.lone = lone_waves(c.d, visible_slots(p, max_len), ((int64_t)total_q * p.group / kFewRowTile + c.nseq) * c.hkv);
-  p.whole = whole_row_tiles(c, p, total_q, max_len);
+  p.lone = lone_waves(c.d, visible, ((int64_t)total_q * p.group / kFewRowTile + c.nseq) * c.hkv);
+  p.whole = few_slots(visible, tiles) || many_even_tiles(c, p, visible, tiles, total_q, max_q) || joins_past_grid(c, p, total_q);
   if (p.any_chunk && !p.whole) {
     p.stat_off = kPlaces * c.d * 4;
     p.begin_off = chunk_area(c);
@@ -584,9 +600,10 @@ size_t kv4_chunk_bytes(const KvView &c, int n_q_heads, int total_q, int window, 
   if (total_q == 0) return 0;
   const ChunkPlan p = kv4_chunk_plan(c, n_q_heads, total_q, window, sinks, max_len, max_q);
   const int fewest = std::min(total_q, kFewRows / p.group + 1);
+  const int64_t visible = visible_slots(p, max_len);
   size_t n = 0;
-  if (p.any_chunk && !whole_row_tiles(c, p, fewest, max_len)) n += chunk_area(c) + begins_area(c);
-  if (!lone_waves(c.d, visible_slots(p, max_len), c.hkv)) n += few_area(c) + begins_area(c);
+  if (p.any_chunk && !few_slots(visible, row_tiles(c, p, fewest)) && !joins_past_grid(c, p, fewest)) n += chunk_area(c) + begins_area(c);
+  if (!lone_waves(c.d, visible, c.hkv)) n += few_area(c) + begins_area(c);
   return n;
 }
 
