@@ -79,7 +79,7 @@ class Rotary:
     * ``{"kind": "yarn", "factor": f, "original": n}``: divided by f for pairs of
       at most beta_slow (1) turns over the n positions of the original context,
       as they are from beta_fast (32) turns on, a ramp over the pairs between;
-      sine and cosine times gain (default 0.1 log f + 1);
+      sine and cosine times gain (default 0.1 log f + 1, and 1 up to f = 1);
     * ``{"kind": "bands", "factor": f, "original": n}``: the same by turns, from
       low (1) to high (4), with the ramp over the turns.
 
