@@ -28,11 +28,14 @@
 // The work is cut into 256 equal shares of a line of tiles (Cut) whose parts a second launch joins, or row tiles are
 // taken whole (few_slots, many_even_tiles).  Sequences of up to 64 rows go to k_kv4_few.
 //
-// Bound: matrix cores and vector issue, which two waves a SIMD overlap in part (matrix cores busy 43 % of the cycles,
-// vector units 51 %, some wave issuing in 92 %, clock 1.95 GHz: the time behaves as the sum of the two); in calls of few
-// tiles the latency of a share and of the second launch.  Measured: 1000 tokens after 30,011, 64/8
-// heads of 128, fp16: 1894 us, 0.53 PFLOP/s of visible pairs (the path that rounds keys: 1010); 512 tokens after 16,001 of
-// 32/8 heads of 128, bf16: 165 us, 0.82 PFLOP/s; of 16/4 heads of 256 205 (fp16 343).
+// Bound: matrix cores and vector issue (matrix cores busy 43 % of the cycles; vector units 51 %, the issue of matrix
+// instructions among it, so the two do not add up; some wave issuing in 92 %; clock 1.95 GHz), which is as far as two waves
+// a SIMD overlapped them: opposite orders, priorities and products between the exponentials of one wave gained nothing
+// more.  In calls of few tiles the latency of a share and of the second launch.  Heads of 256 hold all 256 registers and
+// spill 17 more, for fp16 results 42, of which a tile's loop reads 4 and 34 back.  Measured, median: 1000 tokens after
+// 30,011, 64/8 heads of 128, fp16: 1866 to 1980 us from card to card, 0.53 PFLOP/s of visible pairs (bf16, which rounds
+// keys: 1012); 512 tokens after 16,001 of 32/8 heads of 128, bf16: 163 to 169 us, 0.83 PFLOP/s; of 16/4 heads of 256 186 to
+// 205 (fp16 311 to 343).
 #include <algorithm>
 #include <climits>
 
@@ -469,7 +472,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_chunk(KvView c, ChunkPlan p
 }
 
 // The second launch, of both kernels' cut row tiles: the first `blocks` workgroups take kJoinRows rows each of
-// k_kv4_chunk's (16: 41 us for a mixed batch that took 45 with all 256), the others a row tile each of k_kv4_few's.
+// k_kv4_chunk's (16: 46 us for two chunks beside 30 single tokens of 9/3 heads of 64, fp16, 86 with all 256), the others a row tile each of k_kv4_few's.
 template <int D, bool F16>
 __global__ __launch_bounds__(kJoinThreads) void k_kv4_chunk_join(KvView c, ChunkPlan p, ChunkArgs a, ChunkArgs few, int blocks) {
   int id = blockIdx.x;

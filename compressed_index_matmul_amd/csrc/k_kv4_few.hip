@@ -22,7 +22,8 @@
 //
 // Queries lie in LDS, the same for every wave.  Two tiles in flight a wave gained
 // nothing (64 sequences on 8000 slots: 172 and 173 us), nor three waves a SIMD for heads
-// of 128 (the same on long lengths, 5 to 10 % slower on short ones).
+// of 128 (the same on long lengths, 5 to 10 % slower on short ones).  Heads of 256 in shares
+// spill 2 registers, for fp16 results 8.
 #include <algorithm>
 
 #include "kv4_chunk.h"
