@@ -654,7 +654,9 @@ size_t kv4_attend_workspace_size(const kv4_cache *c, int32_t n_seqs, int32_t n_q
  * VQ_F16 scores are exact but for their sums (queries exact within 2^23 of their
  * head's largest), values are rounded to fp16 and of probabilities the remainder
  * of the rounding takes part too.  A step or minimum that is not finite makes
- * its group of channels NaN for the queries that see the slot.
+ * its group of channels NaN for the queries that see the slot.  A head of a
+ * query that holds a NaN or an infinity gives NaN (where every score is minus
+ * infinity, NaN or the zeros and -inf of a query that sees nothing).
  */
 int kv4_attend_chunk(const kv4_cache *c, const kv4_seqs *s, const attn_heads *q, int32_t dtype, int32_t n_q_heads,
                      int32_t total_q, const int32_t *cu_q, float scale, int32_t window, int32_t sinks, int32_t max_len,
